@@ -173,7 +173,7 @@ def prepare(case, seed):
         from ternary_weight_only_tern_b200 import api
 
         if c["op"] == "linear":
-            s["w"] = api.NibWeight(c["N"], c["K"], c["group"], s["codes"], s["scale"], s["mu"])
+            s["w"] = api.NibWeight(c["N"], c["K"], c["group"], s["codes"], s["scale"], s["mu"], static=True)
         elif c["op"] in ("append", "attention"):
             s["cache"] = api.PagedCache(s["pool"])
     return s
