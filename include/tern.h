@@ -288,6 +288,113 @@ tern_status tern_decode_ranges(const tern_weight* const* w, int32_t n, int64_t M
 tern_status tern_rotate(const tern_half* x, int64_t M, int64_t K, const tern_half* R, tern_half* y,
                         tern_stream stream);
 
+/* ---------------------------------------------------------------- 4-bit weights */
+
+/* A weight W [N, K] in 4 bits, for the layers that a ternary plane costs too much and for the
+ * output head, which the pages keep in 16 bits ("Post-Training Ternarization of Qwen3-4B",
+ * sections 3.1 and 7.3); not on the pages otherwise:
+ *   W[n, k] = mu[n, k / group] + scale[n, k / group] (c[n, k] - 8),  c in 0 .. 15,
+ * with an fp16 scale and, unless mu is NULL, an fp16 offset per (row, group), group 32, 64 or 128.
+ * Strips of 16 rows are laid out in the order in which a warp's matrix fragments take them; the
+ * rows of the last strip past N - 1 are never used (tern_nib_fit and tern_nib_pack zero them):
+ *   codes      uint32 [ceil(N / 16), K / 128, 256]: word ((h 8 + g) 4 + q) 4 + j of a block holds, for
+ *              row 8 h + g of the strip (h < 2, g < 8), columns 32 j + 8 q .. + 7 of the 128
+ *              (q, j < 4), column 2 (p % 4) + p / 4 of the eight at bits 4 p .. 4 p + 3;
+ *   scale, mu  fp16 [ceil(N / 16), K / group, 16], row r of the strip at 2 (r % 8) + r / 8.
+ * Every pointer is device memory, caller-owned, 16-byte aligned.                          */
+typedef struct {
+    int64_t N, K;                /* K % 128 == 0                                         */
+    int32_t group;               /* 32, 64 or 128                                        */
+    uint32_t flags;              /* 0 or TERN_WEIGHT_STATIC, as tern_weight.flags         */
+    const uint32_t* codes;
+    const tern_half* scale;
+    const tern_half* mu;         /* or NULL                                              */
+} tern_nib_weight;
+
+/* Dense fp16 W [N, K] (device) -> codes, scale and, with offset != 0, mu of a tern_nib_weight. Per
+ * (row, group), in fp32 with every operation rounded on its own (rn16: to fp16, to nearest even):
+ *   with an offset  s = rn16((max - min) / 15), mu = rn16(min + 8 s);
+ *   without         s = rn16(max |w| / 7), mu = 0;
+ *   c = clamp(rint((w - mu) / s) + 8, 0, 15), 8 where s = 0.
+ * A group with a NaN or an infinity gets non-finite scales. Asynchronous on `stream`.     */
+tern_status tern_nib_fit(const tern_half* W, int64_t N, int64_t K, int32_t group, int32_t offset, uint32_t* codes,
+                         tern_half* scale, tern_half* mu, tern_stream stream);
+
+/* Row-major 4-bit weights of another source into the strip layout: c uint8 [N, K] (0 .. 15), s fp16
+ * [N, K / group] and, unless NULL, m fp16 [N, K / group] -> codes, scale, mu. A code above 15
+ * is stored as 15 and the call returns TERN_ERR_BAD_CODE. Synchronous on `stream`.          */
+tern_status tern_nib_pack(const uint8_t* c, const tern_half* s, const tern_half* m, int64_t N, int64_t K,
+                          int32_t group, uint32_t* codes, tern_half* scale, tern_half* mu, tern_stream stream);
+
+/* out [N, K] (device) = fp16 of W, each weight rounded once. Asynchronous on `stream`.   */
+tern_status tern_nib_dequant(const tern_nib_weight* w, tern_half* out, tern_stream stream);
+
+/* Bytes of workspace tern_nib_linear needs for this weight and batch size (0 if none).  */
+size_t tern_nib_linear_workspace_bytes(const tern_nib_weight* w, int64_t M);
+
+/* y [M, N] = x [M, K] . W^T (x, y device, fp16, row-major), fp32 accumulation, one rounding to
+ * fp16. Any M >= 0 (0 is a no-op). x and y must not overlap. Workspace rule, streams and capture
+ * as for tern_linear.                                                                     */
+tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half* x, int64_t M, tern_half* y, void* workspace,
+                            size_t workspace_bytes, tern_stream stream);
+
+/* ---------------------------------------------------------------- 4-bit KV cache */
+
+/* Keys and values of past tokens in 4 bits, in pages (the pages leave attention and its cache in 16
+ * bits: "Post-Training Ternarization of Qwen3-4B", section 3.1; next to 2-bit weights the cache is what
+ * a decode step reads most). Per token, head and 64 entries of the head: an fp16 step s and an
+ * fp16 zero z, value = z + s c, c in 0 .. 15. A page holds `page` tokens of every kv head; per
+ * (page, head) it is page / 16 blocks of 16 tokens, 18 head_dim bytes each, D = head_dim:
+ *   K codes   8 D bytes: word ((h 8 + g) 4 + q) D / 32 + j: token 8 h + g, entries 32 j + 8 q .. + 7
+ *             (nibbles as in tern_nib_weight.codes);
+ *   V codes   8 D bytes: word ((h 8 + g) 4 + q) D / 32 + j: tokens 8 h + 2 q (bits 4 p, p = 0 .. 3) and
+ *             8 h + 2 q + 1 (bits 16 + 4 p), entry 16 (2 j + p / 2) + 8 (p % 2) + g;
+ *   K scales  D bytes: fp16 [16 tokens, D / 64, 2] (s, z);
+ *   V scales  D bytes: fp16 [4 q, D / 64, 2 (s, z), 4]: tokens 2 q, 2 q + 1, 2 q + 8, 2 q + 9.
+ * Sequence b's token t lies in page table[b, t / page] (table int32 [B, width], device), at t % page. An
+ * entry outside 0 .. pages - 1, or a t past the table's width, is no page: nothing is written there,
+ * it reads as zeros, and attention does not see it. Pages may be shared by sequences that only
+ * read them; two tokens of one tern_cache_append in the same place leave either.            */
+typedef struct {
+    uint8_t* pool;               /* [pages, kv_heads, page / 16, 18 head_dim], device, 16-byte aligned */
+    int64_t pages;
+    int32_t page;                /* tokens per page: a multiple of 16, at most 65536       */
+    int32_t kv_heads;
+    int32_t head_dim;            /* 64 or 128                                            */
+} tern_cache;
+
+/* Quantises k, v [B, T, kv_heads, head_dim] (device, fp16) into the cache: token t < counts[b] of
+ * sequence b becomes its token start[b] + t (start, counts int32 [B], device; counts NULL: T
+ * each; values outside 0 .. T are taken as the nearer end, a negative start writes nothing before token
+ * 0). Per 64 entries, in fp32 with every operation rounded on its own: s = rn16((max - min) / 15),
+ * z = rn16(min), c = clamp(rint((x - z) / s), 0, 15), 0 where s = 0. Asynchronous on `stream`. */
+tern_status tern_cache_append(const tern_cache* cache, const tern_half* k, const tern_half* v, int64_t B, int64_t T,
+                              const int32_t* table, int64_t width, const int32_t* start, const int32_t* counts,
+                              tern_stream stream);
+
+/* k, v [B, T, kv_heads, head_dim] (device, fp16) = the cached tokens start[b] + t, each value rounded
+ * once; zeros at t >= counts[b] and where there is no page. Asynchronous on `stream`.      */
+tern_status tern_cache_read(const tern_cache* cache, tern_half* k, tern_half* v, int64_t B, int64_t T,
+                            const int32_t* table, int64_t width, const int32_t* start, const int32_t* counts,
+                            tern_stream stream);
+
+/* Bytes of workspace tern_cache_attention needs (0 when the arguments are invalid).       */
+size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, int64_t T, int64_t heads);
+
+/* o [B, T, heads, head_dim] = softmax(scale q K^T + mask) V for the last tokens of each sequence over its
+ * cache (q, o device, fp16): decoding (T = 1), drafted tokens, short chunks; T <= 64. heads is a
+ * multiple of kv_heads; head i reads kv head i / (heads / kv_heads). lens int32 [B]: the cached
+ * tokens of each sequence, the queries' own among them (negative: none). counts int32 [B] or NULL
+ * (T each): sequence b has counts[b] queries (clamped to 0 .. T), query i at token lens[b] - counts[b] +
+ * i; rows of o at i >= counts[b] are left as they were. A query at token p sees token j when
+ * j <= p, and, with window > 0, j > p - window or j < sinks. One that sees nothing gets zeros. Scores,
+ * softmax and sums in fp32, the probabilities rounded to fp16 for the product with V, V to fp16 once.
+ * q and o must not overlap. Workspace rule and capture as for tern_linear.                */
+tern_status tern_cache_attention(const tern_cache* cache, const tern_half* q, int64_t B, int64_t T, int64_t heads,
+                                 const int32_t* table, int64_t width, const int32_t* lens, const int32_t* counts,
+                                 float scale, int64_t window, int64_t sinks, tern_half* o, void* workspace,
+                                 size_t workspace_bytes, tern_stream stream);
+
 /* ---------------------------------------------------------------- bit accounting */
 
 typedef struct {

@@ -8,7 +8,8 @@ imports without PyTorch or the library.
 """
 
 _API = ("TernWeight", "linear", "workspace_bytes", "pack_exec", "unpack_exec", "pack_store",
-        "unpack_store", "weight_validate", "bits")
+        "unpack_store", "weight_validate", "bits", "NibWeight", "nib_fit", "nib_pack", "nib_dequant", "nib_linear",
+        "PagedCache", "cache_append", "cache_read", "cache_attention")
 
 
 def __getattr__(name):

@@ -49,6 +49,22 @@ EXPORTS = {
     "tern_pack_residual": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
     "tern_unpack_residual": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p,
                                         _c.c_void_p]),
+    "tern_nib_fit": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_void_p, _c.c_void_p,
+                                _c.c_void_p, _c.c_void_p]),
+    "tern_nib_pack": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int32,
+                                 _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "tern_nib_dequant": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "tern_nib_linear_workspace_bytes": (_c.c_size_t, [_c.c_void_p, _c.c_int64]),
+    "tern_nib_linear": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_size_t,
+                                   _c.c_void_p]),
+    "tern_cache_append": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                     _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "tern_cache_read": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                   _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "tern_cache_attention_workspace_bytes": (_c.c_size_t, [_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64]),
+    "tern_cache_attention": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p,
+                                        _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_float, _c.c_int64, _c.c_int64,
+                                        _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "tern_device_status": (_c.c_int, [_c.c_void_p]),
     "tern_selftest_timeout": (_c.c_int, [_c.c_int64, _c.c_void_p]),
     "tern_debug_build": (_c.c_int, []),
@@ -68,6 +84,22 @@ class TernWeightC(ctypes.Structure):
         ("ecount", ctypes.c_void_p), ("ebase", ctypes.c_void_p), ("eidx", ctypes.c_void_p),
         ("escale", ctypes.c_void_p), ("nnz2", ctypes.c_int64),
         ("res_per_strip", ctypes.c_void_p),
+    ]
+
+
+class TernNibWeightC(ctypes.Structure):
+    """struct tern_nib_weight."""
+    _fields_ = [
+        ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("group", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("mu", ctypes.c_void_p),
+    ]
+
+
+class TernCacheC(ctypes.Structure):
+    """struct tern_cache."""
+    _fields_ = [
+        ("pool", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
     ]
 
 

@@ -4,6 +4,7 @@ No arithmetic of the method happens here; every step runs in the library's kerne
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -411,6 +412,290 @@ def rotate(x: torch.Tensor, R: torch.Tensor, out: torch.Tensor | None = None) ->
         if tuple(out.shape) != (M, K):
             raise ValueError(f"out must have shape {(M, K)}")
     _lib.check("tern_rotate", _lib.load().tern_rotate(_ptr(x), M, K, _ptr(R), _ptr(out), _stream(x.device)))
+    return out
+
+
+# ------------------------------------------------------------------------------ 4-bit weights
+
+def _on_device(*ts: torch.Tensor):
+    """Checks that the tensors share one CUDA device, and makes it the current one for the call."""
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+NIB_GROUPS = (32, 64, 128)
+
+
+@dataclass
+class NibWeight:
+    """A weight W [N, K] in 4 bits, W = mu + scale (c - 8) per (row, group), in the strip layout of
+    struct tern_nib_weight, on one CUDA device. A new one is made by nib_fit or nib_pack."""
+    N: int
+    K: int
+    group: int               # 32, 64 or 128
+    codes: torch.Tensor      # int32 [ceil(N/16), K/128, 256]
+    scale: torch.Tensor      # float16 [ceil(N/16), K/group, 16]
+    mu: torch.Tensor | None = None   # float16 as scale, or None
+    static: bool = False     # weights not written by queued work: nib_linear may read them early
+
+    def __post_init__(self):
+        if self.group not in NIB_GROUPS:
+            raise ValueError(f"group must be one of {NIB_GROUPS}, got {self.group}")
+        if self.N <= 0 or self.K <= 0 or self.K % GROUP:
+            raise ValueError("N must be positive and K a positive multiple of 128")
+        strips = -(-self.N // 16)
+        for t, dt, name, shape in ((self.codes, torch.int32, "codes", (strips, self.K // GROUP, 256)),
+                                   (self.scale, torch.float16, "scale", (strips, self.K // self.group, 16)),
+                                   (self.mu, torch.float16, "mu", (strips, self.K // self.group, 16))):
+            if t is None and name == "mu":
+                continue
+            _need(t, dt, name, ndim=3)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+            if t.device != self.codes.device:
+                raise ValueError("codes, scale and mu must share one device")
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def __setattr__(self, name, value):
+        # a changed field drops the cached C descriptor and workspace sizes
+        object.__setattr__(self, name, value)
+        if name not in ("_c", "_ws"):
+            object.__setattr__(self, "_c", None)
+            object.__setattr__(self, "_ws", None)
+
+    def c_struct(self) -> _lib.TernNibWeightC:
+        c = getattr(self, "_c", None)
+        if c is None:
+            c = _lib.TernNibWeightC(self.N, self.K, self.group, _lib.WEIGHT_STATIC if self.static else 0,
+                                    self.codes.data_ptr(), self.scale.data_ptr(),
+                                    self.mu.data_ptr() if self.mu is not None else None)
+            object.__setattr__(self, "_c", c)
+        return c
+
+    def nbytes(self) -> int:
+        """Bytes held: codes, scales and offsets."""
+        return sum(t.numel() * t.element_size() for t in (self.codes, self.scale, self.mu) if t is not None)
+
+
+def _nib_empty(N: int, K: int, group: int, offset: bool, device) -> NibWeight:
+    if group not in NIB_GROUPS:
+        raise ValueError(f"group must be one of {NIB_GROUPS}, got {group}")
+    if N <= 0 or K <= 0 or K % GROUP:
+        raise ValueError("N must be positive and K a positive multiple of 128")
+    strips = -(-N // 16)
+    new = lambda *shape, dt=torch.float16: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+    return NibWeight(N, K, group, new(strips, K // GROUP, 256, dt=torch.int32), new(strips, K // group, 16),
+                     new(strips, K // group, 16) if offset else None)
+
+
+def nib_fit(W: torch.Tensor, group: int = GROUP, offset: bool = True) -> NibWeight:
+    """Dense fp16 W [N, K] -> 4-bit weight by tern_nib_fit, with a per-group offset or symmetric."""
+    _need(W, torch.float16, "W")
+    w = _nib_empty(*W.shape, group, offset, W.device)
+    with _on_device(W):
+        _lib.check("tern_nib_fit", _lib.load().tern_nib_fit(
+            _ptr(W), w.N, w.K, group, int(offset), _ptr(w.codes), _ptr(w.scale), _ptr(w.mu), _stream(W.device)))
+    return w
+
+
+def nib_pack(codes: torch.Tensor, scale: torch.Tensor, mu: torch.Tensor | None = None) -> NibWeight:
+    """Row-major codes uint8 [N, K] in 0 .. 15 with scale (and mu) fp16 [N, K/group] -> 4-bit weight."""
+    _need(codes, torch.uint8, "codes")
+    N, K = codes.shape
+    for t, name in ((scale, "scale"), (mu, "mu")):
+        if t is None and name == "mu":
+            continue
+        _need(t, torch.float16, name)
+        if t.shape[0] != N or t.shape[1] == 0 or K % t.shape[1] or tuple(t.shape) != tuple(scale.shape):
+            raise ValueError(f"{name} must have shape ({N}, K/group), got {tuple(t.shape)}")
+    w = _nib_empty(N, K, K // scale.shape[1], mu is not None, codes.device)
+    with _on_device(*(t for t in (codes, scale, mu) if t is not None)):
+        _lib.check("tern_nib_pack", _lib.load().tern_nib_pack(
+            _ptr(codes), _ptr(scale), _ptr(mu), N, K, w.group, _ptr(w.codes), _ptr(w.scale), _ptr(w.mu),
+            _stream(codes.device)))
+    return w
+
+
+def nib_dequant(w: NibWeight, out: torch.Tensor | None = None) -> torch.Tensor:
+    """fp16 W [N, K] of a 4-bit weight."""
+    if out is None:
+        out = torch.empty((w.N, w.K), dtype=torch.float16, device=w.device)
+    else:
+        _need(out, torch.float16, "out")
+        if tuple(out.shape) != (w.N, w.K):
+            raise ValueError(f"out must have shape {(w.N, w.K)}, got {tuple(out.shape)}")
+    with _on_device(w.codes, out):
+        _lib.check("tern_nib_dequant", _lib.load().tern_nib_dequant(ctypes.byref(w.c_struct()), _ptr(out),
+                                                                    _stream(out.device)))
+    return out
+
+
+def nib_workspace_bytes(w: NibWeight, M: int) -> int:
+    """tern_nib_linear_workspace_bytes, remembered per weight and M."""
+    cache = getattr(w, "_ws", None)
+    if cache is None:
+        cache = {}
+        object.__setattr__(w, "_ws", cache)
+    n = cache.get(M)
+    if n is None:
+        with _on_device(w.codes):
+            n = cache[M] = int(_lib.load().tern_nib_linear_workspace_bytes(ctypes.byref(w.c_struct()), M))
+    return n
+
+
+def _scratch(workspace: torch.Tensor | None, need: int, device) -> tuple:
+    """The caller's workspace where it is large enough, else one of the call's own, and its bytes."""
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.device != device:
+            raise ValueError(f"workspace must be on {device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def nib_linear(x: torch.Tensor, w: NibWeight, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y [M, N] = x [M, K] . W^T for a 4-bit W (fp16 in, fp32 accumulation, fp16 out)."""
+    _need(x, torch.float16, "x")
+    M, K = x.shape
+    if K != w.K:
+        raise ValueError(f"x has K={K}, weight has K={w.K}")
+    if out is None:
+        out = torch.empty((M, w.N), dtype=torch.float16, device=x.device)
+    else:
+        _need(out, torch.float16, "out")
+        if tuple(out.shape) != (M, w.N):
+            raise ValueError(f"out must have shape {(M, w.N)}, got {tuple(out.shape)}")
+    workspace, ws_bytes = _scratch(workspace, nib_workspace_bytes(w, M), x.device)
+    with _on_device(x, w.codes, out):
+        _lib.check("tern_nib_linear", _lib.load().tern_nib_linear(
+            ctypes.byref(w.c_struct()), _ptr(x), M, _ptr(out), _ptr(workspace), ws_bytes, _stream(x.device)))
+    return out
+
+
+# ------------------------------------------------------------------------------ 4-bit KV cache
+
+class PagedCache:
+    """Keys and values of past tokens in 4 bits, in pages (struct tern_cache): pool uint8
+    [pages, kv_heads, page / 16, 18 head_dim]. Which page holds which tokens of which sequence is said by
+    the table of each call, int32 [B, width]: sequence b's token t is in page table[b, t // page], at t % page;
+    an entry outside the pool is no page."""
+
+    def __init__(self, pool: torch.Tensor):
+        _need(pool, torch.uint8, "pool", ndim=4)
+        self.pages, self.kv_heads, blocks, unit = pool.shape
+        if unit not in (18 * 64, 18 * 128) or not pool.numel():
+            raise ValueError("pool must have shape (pages, kv_heads, page / 16, 18 head_dim), head_dim 64 or 128")
+        self.pool, self.page, self.head_dim = pool, 16 * blocks, unit // 18
+        self._c = _lib.TernCacheC(pool.data_ptr(), self.pages, self.page, self.kv_heads, self.head_dim)
+        self._ws = {}
+
+    @classmethod
+    def empty(cls, pages: int, page: int, kv_heads: int, head_dim: int, device="cuda") -> "PagedCache":
+        """A cache of `pages` pages of `page` tokens (a multiple of 16), zeroed."""
+        if page <= 0 or page % 16:
+            raise ValueError("page must be a positive multiple of 16")
+        return cls(torch.zeros((pages, kv_heads, page // 16, 18 * head_dim), dtype=torch.uint8, device=device))
+
+    @property
+    def device(self) -> torch.device:
+        return self.pool.device
+
+    def nbytes(self) -> int:
+        return self.pool.numel()
+
+    def workspace_bytes(self, B: int, T: int, heads: int) -> int:
+        """tern_cache_attention_workspace_bytes, remembered per size."""
+        n = self._ws.get((B, T, heads))
+        if n is None:
+            with _on_device(self.pool):
+                n = self._ws[B, T, heads] = int(_lib.load().tern_cache_attention_workspace_bytes(
+                    ctypes.byref(self._c), B, T, heads))
+        return n
+
+
+def _batch(cache: PagedCache, table: torch.Tensor, B: int, *others) -> list:
+    """Checks the table and the int32 [B] tensors (name, tensor or None) of a call; the tensors given."""
+    _need(table, torch.int32, "table")
+    if table.shape[0] != B:
+        raise ValueError(f"table must have {B} rows, got {table.shape[0]}")
+    given = [cache.pool, table]
+    for name, t in others:
+        if t is None:
+            continue
+        _need(t, torch.int32, name, ndim=1)
+        if t.shape[0] != B:
+            raise ValueError(f"{name} must have {B} entries, got {t.shape[0]}")
+        given.append(t)
+    return given
+
+
+def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
+                 counts: torch.Tensor | None = None) -> None:
+    """Quantises k, v fp16 [B, T, kv_heads, head_dim] into the cache: token t < counts[b] (T without
+    counts) of sequence b becomes its token start[b] + t."""
+    _need(k, torch.float16, "k", ndim=4)
+    _need(v, torch.float16, "v", ndim=4)
+    B, T = k.shape[:2]
+    if v.shape != k.shape or tuple(k.shape[2:]) != (cache.kv_heads, cache.head_dim):
+        raise ValueError(f"k and v must have shape (B, T, {cache.kv_heads}, {cache.head_dim})")
+    with _on_device(*_batch(cache, table, B, ("start", start), ("counts", counts)), k, v):
+        _lib.check("tern_cache_append", _lib.load().tern_cache_append(
+            ctypes.byref(cache._c), _ptr(k), _ptr(v), B, T, _ptr(table), table.shape[1], _ptr(start), _ptr(counts),
+            _stream(k.device)))
+
+
+def cache_read(cache: PagedCache, table: torch.Tensor, start: torch.Tensor, T: int,
+               counts: torch.Tensor | None = None, out: tuple | None = None) -> tuple:
+    """(k, v) fp16 [B, T, kv_heads, head_dim]: the cached tokens start[b] + t, zeros at t >= counts[b] and
+    where there is no page."""
+    B = table.shape[0]
+    shape = (B, T, cache.kv_heads, cache.head_dim)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=torch.float16, device=cache.device) for _ in range(2))
+    k, v = out
+    for t, name in ((k, "out[0]"), (v, "out[1]")):
+        _need(t, torch.float16, name, ndim=4)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    with _on_device(*_batch(cache, table, B, ("start", start), ("counts", counts)), k, v):
+        _lib.check("tern_cache_read", _lib.load().tern_cache_read(
+            ctypes.byref(cache._c), _ptr(k), _ptr(v), B, T, _ptr(table), table.shape[1], _ptr(start), _ptr(counts),
+            _stream(cache.device)))
+    return k, v
+
+
+def cache_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, lens: torch.Tensor,
+                    counts: torch.Tensor | None = None, scale: float | None = None, window: int = 0, sinks: int = 0,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """o [B, T, heads, head_dim] = softmax(scale q K^T + mask) V, q fp16 [B, T, heads, head_dim], T <= 64, over each
+    sequence's lens[b] cached tokens, of which its queries are the last counts[b] (T without counts;
+    rows behind them are left as they were). Causal; with window > 0 a query sees the last `window` tokens up to its
+    own and the first `sinks`. scale: 1 / sqrt(head_dim) by default."""
+    _need(q, torch.float16, "q", ndim=4)
+    B, T, heads, D = q.shape
+    if D != cache.head_dim or heads % cache.kv_heads or not heads:
+        raise ValueError(f"q must have shape (B, T, a multiple of {cache.kv_heads}, {cache.head_dim})")
+    if out is None:
+        out = torch.empty_like(q) if counts is None else torch.zeros_like(q)
+    else:
+        _need(out, torch.float16, "out", ndim=4)
+        if out.shape != q.shape:
+            raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    workspace, ws_bytes = _scratch(workspace, cache.workspace_bytes(B, T, heads), q.device)
+    with _on_device(*_batch(cache, table, B, ("lens", lens), ("counts", counts)), q, out):
+        _lib.check("tern_cache_attention", _lib.load().tern_cache_attention(
+            ctypes.byref(cache._c), _ptr(q), B, T, heads, _ptr(table), table.shape[1], _ptr(lens), _ptr(counts),
+            D ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(workspace), ws_bytes,
+            _stream(q.device)))
     return out
 
 
