@@ -357,7 +357,7 @@ tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half* x, int64_
  * read them; two tokens of one tern_cache_append in the same place leave either.            */
 typedef struct {
     uint8_t* pool;               /* [pages, kv_heads, page / 16, 18 head_dim], device, 16-byte aligned */
-    int64_t pages;
+    int64_t pages;               /* pages kv_heads page / 16 < 2^31                       */
     int32_t page;                /* tokens per page: a multiple of 16, at most 65536       */
     int32_t kv_heads;
     int32_t head_dim;            /* 64 or 128                                            */

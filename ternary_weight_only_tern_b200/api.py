@@ -4,7 +4,6 @@ No arithmetic of the method happens here; every step runs in the library's kerne
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -417,13 +416,42 @@ def rotate(x: torch.Tensor, R: torch.Tensor, out: torch.Tensor | None = None) ->
 
 # ------------------------------------------------------------------------------ 4-bit weights
 
-def _on_device(*ts: torch.Tensor):
-    """Checks that the tensors share one CUDA device, and makes it the current one for the call."""
-    dev = ts[0].device
-    for t in ts[1:]:
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+# These calls decide a decode step's time on the host, so each tensor is checked by one expression and the reason
+# looked for only when it fails; pointers go to ctypes as plain integers.
+_F16, _I32 = torch.float16, torch.int32
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_of(dev: int) -> int:
+    """The current stream of device number dev, as an integer."""
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _refuse(t, dtype, name: str, ndim: int, dev: int):
+    """Raises for a tensor that is not contiguous, of that type and dims, on that device."""
+    _need(t, dtype, name, ndim)
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _at(t: torch.Tensor, dtype, name: str, ndim: int, dev: int) -> int:
+    """The tensor's address, once checked."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or t.get_device() != dev or dev < 0 \
+            or not t.is_contiguous():
+        _refuse(t, dtype, name, ndim, dev)
+    return t.data_ptr()
+
+
+def _scratch(workspace: torch.Tensor | None, need: int, like: torch.Tensor) -> tuple:
+    """(tensor, bytes): the caller's workspace where it is large enough, else one of the call's own."""
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.get_device() != like.get_device():
+            raise ValueError(f"workspace must be on {like.device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        have = workspace.numel() * workspace.element_size()
+        if have >= need:
+            return workspace, have
+    return like.new_empty(need, dtype=torch.uint8), need
 
 
 NIB_GROUPS = (32, 64, 128)
@@ -442,10 +470,7 @@ class NibWeight:
     static: bool = False     # weights not written by queued work: nib_linear may read them early
 
     def __post_init__(self):
-        if self.group not in NIB_GROUPS:
-            raise ValueError(f"group must be one of {NIB_GROUPS}, got {self.group}")
-        if self.N <= 0 or self.K <= 0 or self.K % GROUP:
-            raise ValueError("N must be positive and K a positive multiple of 128")
+        _nib_check_shape(self.N, self.K, self.group)
         strips = -(-self.N // 16)
         for t, dt, name, shape in ((self.codes, torch.int32, "codes", (strips, self.K // GROUP, 256)),
                                    (self.scale, torch.float16, "scale", (strips, self.K // self.group, 16)),
@@ -463,121 +488,138 @@ class NibWeight:
         return self.codes.device
 
     def __setattr__(self, name, value):
-        # a changed field drops the cached C descriptor and workspace sizes
-        object.__setattr__(self, name, value)
-        if name not in ("_c", "_ws"):
-            object.__setattr__(self, "_c", None)
-            object.__setattr__(self, "_ws", None)
+        # a changed field drops what is remembered of the weight
+        self.__dict__[name] = value
+        self.__dict__["_seen"] = None
 
-    def c_struct(self) -> _lib.TernNibWeightC:
-        c = getattr(self, "_c", None)
-        if c is None:
+    def _known(self) -> tuple:
+        """(C descriptor, reference to it, device number, workspace bytes by M), remembered until a field changes."""
+        k = self.__dict__.get("_seen")
+        if k is None:
             c = _lib.TernNibWeightC(self.N, self.K, self.group, _lib.WEIGHT_STATIC if self.static else 0,
                                     self.codes.data_ptr(), self.scale.data_ptr(),
                                     self.mu.data_ptr() if self.mu is not None else None)
-            object.__setattr__(self, "_c", c)
-        return c
+            k = self.__dict__["_seen"] = (c, ctypes.byref(c), self.codes.get_device(), {})
+        return k
+
+    def c_struct(self) -> _lib.TernNibWeightC:
+        return self._known()[0]
 
     def nbytes(self) -> int:
         """Bytes held: codes, scales and offsets."""
         return sum(t.numel() * t.element_size() for t in (self.codes, self.scale, self.mu) if t is not None)
 
 
-def _nib_empty(N: int, K: int, group: int, offset: bool, device) -> NibWeight:
+def _nib_check_shape(N: int, K: int, group: int):
     if group not in NIB_GROUPS:
         raise ValueError(f"group must be one of {NIB_GROUPS}, got {group}")
     if N <= 0 or K <= 0 or K % GROUP:
         raise ValueError("N must be positive and K a positive multiple of 128")
+
+
+def _nib_empty(N: int, K: int, group: int, offset: bool, like: torch.Tensor) -> NibWeight:
+    _nib_check_shape(N, K, group)
     strips = -(-N // 16)
-    new = lambda *shape, dt=torch.float16: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
-    return NibWeight(N, K, group, new(strips, K // GROUP, 256, dt=torch.int32), new(strips, K // group, 16),
-                     new(strips, K // group, 16) if offset else None)
+    w = NibWeight.__new__(NibWeight)       # of the right shapes by construction
+    w.__dict__.update(N=N, K=K, group=group, codes=like.new_empty((strips, K // GROUP, 256), dtype=_I32),
+                      scale=like.new_empty((strips, K // group, 16), dtype=_F16),
+                      mu=like.new_empty((strips, K // group, 16), dtype=_F16) if offset else None, static=False)
+    return w
 
 
 def nib_fit(W: torch.Tensor, group: int = GROUP, offset: bool = True) -> NibWeight:
     """Dense fp16 W [N, K] -> 4-bit weight by tern_nib_fit, with a per-group offset or symmetric."""
-    _need(W, torch.float16, "W")
-    w = _nib_empty(*W.shape, group, offset, W.device)
-    with _on_device(W):
-        _lib.check("tern_nib_fit", _lib.load().tern_nib_fit(
-            _ptr(W), w.N, w.K, group, int(offset), _ptr(w.codes), _ptr(w.scale), _ptr(w.mu), _stream(W.device)))
+    dev = W.get_device()
+    at = _at(W, _F16, "W", 2, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return nib_fit(W, group, offset)
+    N, K = W.shape
+    w = _nib_empty(N, K, group, offset, W)
+    s = _lib.load().tern_nib_fit(at, N, K, group, 1 if offset else 0, w.codes.data_ptr(), w.scale.data_ptr(),
+                                 w.mu.data_ptr() if offset else None, _stream_of(dev))
+    if s:
+        _lib.check("tern_nib_fit", s)
     return w
 
 
 def nib_pack(codes: torch.Tensor, scale: torch.Tensor, mu: torch.Tensor | None = None) -> NibWeight:
     """Row-major codes uint8 [N, K] in 0 .. 15 with scale (and mu) fp16 [N, K/group] -> 4-bit weight."""
-    _need(codes, torch.uint8, "codes")
+    dev = codes.get_device()
+    _at(codes, torch.uint8, "codes", 2, dev)
     N, K = codes.shape
     for t, name in ((scale, "scale"), (mu, "mu")):
         if t is None and name == "mu":
             continue
-        _need(t, torch.float16, name)
-        if t.shape[0] != N or t.shape[1] == 0 or K % t.shape[1] or tuple(t.shape) != tuple(scale.shape):
+        _at(t, _F16, name, 2, dev)
+        if t.shape[0] != N or t.shape[1] == 0 or K % t.shape[1] or t.shape != scale.shape:
             raise ValueError(f"{name} must have shape ({N}, K/group), got {tuple(t.shape)}")
-    w = _nib_empty(N, K, K // scale.shape[1], mu is not None, codes.device)
-    with _on_device(*(t for t in (codes, scale, mu) if t is not None)):
+    w = _nib_empty(N, K, K // scale.shape[1], mu is not None, codes)
+    with torch.cuda.device(dev):
         _lib.check("tern_nib_pack", _lib.load().tern_nib_pack(
             _ptr(codes), _ptr(scale), _ptr(mu), N, K, w.group, _ptr(w.codes), _ptr(w.scale), _ptr(w.mu),
-            _stream(codes.device)))
+            _stream_of(dev)))
     return w
 
 
 def nib_dequant(w: NibWeight, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp16 W [N, K] of a 4-bit weight."""
+    _, ref, dev, _ = w._known()
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return nib_dequant(w, out)
     if out is None:
-        out = torch.empty((w.N, w.K), dtype=torch.float16, device=w.device)
+        out = w.scale.new_empty((w.N, w.K))
+        at = out.data_ptr()
     else:
-        _need(out, torch.float16, "out")
-        if tuple(out.shape) != (w.N, w.K):
+        at = _at(out, _F16, "out", 2, dev)
+        if out.shape != (w.N, w.K):
             raise ValueError(f"out must have shape {(w.N, w.K)}, got {tuple(out.shape)}")
-    with _on_device(w.codes, out):
-        _lib.check("tern_nib_dequant", _lib.load().tern_nib_dequant(ctypes.byref(w.c_struct()), _ptr(out),
-                                                                    _stream(out.device)))
+    s = _lib.load().tern_nib_dequant(ref, at, _stream_of(dev))
+    if s:
+        _lib.check("tern_nib_dequant", s)
     return out
 
 
 def nib_workspace_bytes(w: NibWeight, M: int) -> int:
     """tern_nib_linear_workspace_bytes, remembered per weight and M."""
-    cache = getattr(w, "_ws", None)
-    if cache is None:
-        cache = {}
-        object.__setattr__(w, "_ws", cache)
-    n = cache.get(M)
+    _, ref, dev, sizes = w._known()
+    n = sizes.get(M)
     if n is None:
-        with _on_device(w.codes):
-            n = cache[M] = int(_lib.load().tern_nib_linear_workspace_bytes(ctypes.byref(w.c_struct()), M))
+        with torch.cuda.device(dev):
+            n = sizes[M] = int(_lib.load().tern_nib_linear_workspace_bytes(ref, M))
     return n
-
-
-def _scratch(workspace: torch.Tensor | None, need: int, device) -> tuple:
-    """The caller's workspace where it is large enough, else one of the call's own, and its bytes."""
-    if workspace is not None:
-        if not workspace.is_cuda or workspace.device != device:
-            raise ValueError(f"workspace must be on {device}")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def nib_linear(x: torch.Tensor, w: NibWeight, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y [M, N] = x [M, K] . W^T for a 4-bit W (fp16 in, fp32 accumulation, fp16 out)."""
-    _need(x, torch.float16, "x")
+    _need(x, _F16, "x") if not isinstance(w, NibWeight) else None
+    _, ref, dev, sizes = w._known()
+    at = _at(x, _F16, "x", 2, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return nib_linear(x, w, out, workspace)
     M, K = x.shape
     if K != w.K:
         raise ValueError(f"x has K={K}, weight has K={w.K}")
     if out is None:
-        out = torch.empty((M, w.N), dtype=torch.float16, device=x.device)
+        out = x.new_empty((M, w.N))
+        to = out.data_ptr()
     else:
-        _need(out, torch.float16, "out")
-        if tuple(out.shape) != (M, w.N):
+        to = _at(out, _F16, "out", 2, dev)
+        if out.shape != (M, w.N):
             raise ValueError(f"out must have shape {(M, w.N)}, got {tuple(out.shape)}")
-    workspace, ws_bytes = _scratch(workspace, nib_workspace_bytes(w, M), x.device)
-    with _on_device(x, w.codes, out):
-        _lib.check("tern_nib_linear", _lib.load().tern_nib_linear(
-            ctypes.byref(w.c_struct()), _ptr(x), M, _ptr(out), _ptr(workspace), ws_bytes, _stream(x.device)))
+    need = sizes.get(M)
+    if need is None:
+        need = nib_workspace_bytes(w, M)
+    ws = wsb = 0
+    if need or workspace is not None:
+        workspace, wsb = _scratch(workspace, need, x)
+        ws = workspace.data_ptr()
+    s = _lib.load().tern_nib_linear(ref, at, M, to, ws, wsb, _stream_of(dev))
+    if s:
+        _lib.check("tern_nib_linear", s)
     return out
 
 
@@ -596,6 +638,7 @@ class PagedCache:
             raise ValueError("pool must have shape (pages, kv_heads, page / 16, 18 head_dim), head_dim 64 or 128")
         self.pool, self.page, self.head_dim = pool, 16 * blocks, unit // 18
         self._c = _lib.TernCacheC(pool.data_ptr(), self.pages, self.page, self.kv_heads, self.head_dim)
+        self._ref, self._dev = ctypes.byref(self._c), pool.get_device()
         self._ws = {}
 
     @classmethod
@@ -616,60 +659,72 @@ class PagedCache:
         """tern_cache_attention_workspace_bytes, remembered per size."""
         n = self._ws.get((B, T, heads))
         if n is None:
-            with _on_device(self.pool):
-                n = self._ws[B, T, heads] = int(_lib.load().tern_cache_attention_workspace_bytes(
-                    ctypes.byref(self._c), B, T, heads))
+            with torch.cuda.device(self._dev):
+                n = self._ws[B, T, heads] = int(_lib.load().tern_cache_attention_workspace_bytes(self._ref, B, T, heads))
         return n
 
 
-def _batch(cache: PagedCache, table: torch.Tensor, B: int, *others) -> list:
-    """Checks the table and the int32 [B] tensors (name, tensor or None) of a call; the tensors given."""
-    _need(table, torch.int32, "table")
-    if table.shape[0] != B:
-        raise ValueError(f"table must have {B} rows, got {table.shape[0]}")
-    given = [cache.pool, table]
-    for name, t in others:
-        if t is None:
-            continue
-        _need(t, torch.int32, name, ndim=1)
-        if t.shape[0] != B:
-            raise ValueError(f"{name} must have {B} entries, got {t.shape[0]}")
-        given.append(t)
-    return given
+def _per_sequence(t: torch.Tensor | None, name: str, B: int, dev: int):
+    """Address of an int32 [B] tensor, or None."""
+    if t is None:
+        return None
+    at = _at(t, _I32, name, 1, dev)
+    if t.shape[0] != B:
+        raise ValueError(f"{name} must have {B} entries, got {t.shape[0]}")
+    return at
+
+
+def _table(table: torch.Tensor, B: int, dev: int) -> tuple:
+    at = _at(table, _I32, "table", 2, dev)
+    rows, width = table.shape
+    if rows != B:
+        raise ValueError(f"table must have {B} rows, got {rows}")
+    return at, width
 
 
 def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
                  counts: torch.Tensor | None = None) -> None:
     """Quantises k, v fp16 [B, T, kv_heads, head_dim] into the cache: token t < counts[b] (T without
     counts) of sequence b becomes its token start[b] + t."""
-    _need(k, torch.float16, "k", ndim=4)
-    _need(v, torch.float16, "v", ndim=4)
-    B, T = k.shape[:2]
-    if v.shape != k.shape or tuple(k.shape[2:]) != (cache.kv_heads, cache.head_dim):
+    dev = cache._dev
+    ka, va = _at(k, _F16, "k", 4, dev), _at(v, _F16, "v", 4, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return cache_append(cache, k, v, table, start, counts)
+    B, T, heads, D = k.shape
+    if v.shape != k.shape or heads != cache.kv_heads or D != cache.head_dim:
         raise ValueError(f"k and v must have shape (B, T, {cache.kv_heads}, {cache.head_dim})")
-    with _on_device(*_batch(cache, table, B, ("start", start), ("counts", counts)), k, v):
-        _lib.check("tern_cache_append", _lib.load().tern_cache_append(
-            ctypes.byref(cache._c), _ptr(k), _ptr(v), B, T, _ptr(table), table.shape[1], _ptr(start), _ptr(counts),
-            _stream(k.device)))
+    ta, width = _table(table, B, dev)
+    s = _lib.load().tern_cache_append(cache._ref, ka, va, B, T, ta, width, _per_sequence(start, "start", B, dev),
+                                      _per_sequence(counts, "counts", B, dev), _stream_of(dev))
+    if s:
+        _lib.check("tern_cache_append", s)
 
 
 def cache_read(cache: PagedCache, table: torch.Tensor, start: torch.Tensor, T: int,
                counts: torch.Tensor | None = None, out: tuple | None = None) -> tuple:
     """(k, v) fp16 [B, T, kv_heads, head_dim]: the cached tokens start[b] + t, zeros at t >= counts[b] and
     where there is no page."""
+    dev = cache._dev
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return cache_read(cache, table, start, T, counts, out)
     B = table.shape[0]
+    ta, width = _table(table, B, dev)
     shape = (B, T, cache.kv_heads, cache.head_dim)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=torch.float16, device=cache.device) for _ in range(2))
-    k, v = out
-    for t, name in ((k, "out[0]"), (v, "out[1]")):
-        _need(t, torch.float16, name, ndim=4)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    with _on_device(*_batch(cache, table, B, ("start", start), ("counts", counts)), k, v):
-        _lib.check("tern_cache_read", _lib.load().tern_cache_read(
-            ctypes.byref(cache._c), _ptr(k), _ptr(v), B, T, _ptr(table), table.shape[1], _ptr(start), _ptr(counts),
-            _stream(cache.device)))
+        k, v = table.new_empty(shape, dtype=_F16), table.new_empty(shape, dtype=_F16)
+    else:
+        k, v = out
+        for t, name in ((k, "out[0]"), (v, "out[1]")):
+            _at(t, _F16, name, 4, dev)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    s = _lib.load().tern_cache_read(cache._ref, k.data_ptr(), v.data_ptr(), B, T, ta, width,
+                                    _per_sequence(start, "start", B, dev), _per_sequence(counts, "counts", B, dev),
+                                    _stream_of(dev))
+    if s:
+        _lib.check("tern_cache_read", s)
     return k, v
 
 
@@ -680,22 +735,35 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, len
     sequence's lens[b] cached tokens, of which its queries are the last counts[b] (T without counts;
     rows behind them are left as they were). Causal; with window > 0 a query sees the last `window` tokens up to its
     own and the first `sinks`. scale: 1 / sqrt(head_dim) by default."""
-    _need(q, torch.float16, "q", ndim=4)
+    dev = cache._dev
+    qa = _at(q, _F16, "q", 4, dev)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return cache_attention(q, cache, table, lens, counts, scale, window, sinks, out, workspace)
     B, T, heads, D = q.shape
     if D != cache.head_dim or heads % cache.kv_heads or not heads:
         raise ValueError(f"q must have shape (B, T, a multiple of {cache.kv_heads}, {cache.head_dim})")
     if out is None:
         out = torch.empty_like(q) if counts is None else torch.zeros_like(q)
+        to = out.data_ptr()
     else:
-        _need(out, torch.float16, "out", ndim=4)
+        to = _at(out, _F16, "out", 4, dev)
         if out.shape != q.shape:
             raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    workspace, ws_bytes = _scratch(workspace, cache.workspace_bytes(B, T, heads), q.device)
-    with _on_device(*_batch(cache, table, B, ("lens", lens), ("counts", counts)), q, out):
-        _lib.check("tern_cache_attention", _lib.load().tern_cache_attention(
-            ctypes.byref(cache._c), _ptr(q), B, T, heads, _ptr(table), table.shape[1], _ptr(lens), _ptr(counts),
-            D ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(workspace), ws_bytes,
-            _stream(q.device)))
+    ta, width = _table(table, B, dev)
+    need = cache._ws.get((B, T, heads))
+    if need is None:
+        need = cache.workspace_bytes(B, T, heads)
+    ws = wsb = 0
+    if need or workspace is not None:
+        workspace, wsb = _scratch(workspace, need, q)
+        ws = workspace.data_ptr()
+    s = _lib.load().tern_cache_attention(
+        cache._ref, qa, B, T, heads, ta, width, _per_sequence(lens, "lens", B, dev),
+        _per_sequence(counts, "counts", B, dev), D ** -0.5 if scale is None else scale, window, sinks, to, ws, wsb,
+        _stream_of(dev))
+    if s:
+        _lib.check("tern_cache_attention", s)
     return out
 
 

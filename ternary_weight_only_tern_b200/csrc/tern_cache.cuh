@@ -25,14 +25,20 @@ struct Pool {
     int per_page;       // blocks per page
     int heads;
 
-    // Block `blk` (tokens 16 blk ..) of sequence b and kv head h, or nullptr where there is no page.
+    // Place in the pool of block `blk` (tokens 16 blk ..) of sequence b and kv head h, counted in blocks, or -1 where there
+    // is no page (check_cache keeps the count below 2^31).
+    __device__ __forceinline__ int place(int64_t b, int h, int64_t blk) const {
+        const int64_t col = blk < 0x7fffffff ? int64_t(uint32_t(blk) / uint32_t(per_page)) : blk / per_page;
+        if (blk < 0 || col >= width) return -1;
+        const int page = __ldg(table + b * width + col);
+        if (page < 0 || page >= pages) return -1;
+        return (page * heads + h) * per_page + int(blk - col * per_page);
+    }
+
     template <int D>
     __device__ __forceinline__ uint8_t* block(int64_t b, int h, int64_t blk) const {
-        const int64_t col = blk / per_page;
-        if (blk < 0 || col >= width) return nullptr;
-        const int64_t page = __ldg(table + b * width + col);
-        if (page < 0 || page >= pages) return nullptr;
-        return pool + ((page * heads + h) * per_page + (blk - col * per_page)) * unit_bytes(D);
+        const int at = place(b, h, blk);
+        return at < 0 ? nullptr : pool + int64_t(at) * unit_bytes(D);
     }
 };
 
@@ -41,6 +47,7 @@ inline tern_status check_cache(const tern_cache* c) {
     if (c->pages <= 0 || c->pages > 0x7fffffff || c->page <= 0 || c->page % kTok || c->page > 65536 ||
         c->kv_heads <= 0 || c->kv_heads > 65535 || (c->head_dim != 64 && c->head_dim != 128))
         return TERN_ERR_SHAPE;
+    if (c->pages > 0x7fffffff / (int64_t(c->kv_heads) * (c->page / kTok))) return TERN_ERR_SHAPE;   // blocks are counted in int32
     if (!c->pool) return TERN_ERR_NULL;
     return aligned16(c->pool) ? TERN_OK : TERN_ERR_ALIGN;
 }

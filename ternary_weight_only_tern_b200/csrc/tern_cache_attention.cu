@@ -3,15 +3,26 @@
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q k_j - max),  k_j = z + s c (per 64 entries), v_j likewise.
 //
 // The queries that share a kv head (heads / kv_heads of them for each of the T tokens) are the rows, in tiles
-// of 8. A warp takes blocks of 16 cached tokens and runs both products on mma.sync m16n8k16 with the rows as
+// of 8 NT. A warp takes blocks of 16 cached tokens and runs both products on mma.sync m16n8k16 with the rows as
 // the instruction's 8 columns:
 //   S^T [16 tokens, 8 rows] = C_K [16 tokens, D] Q^T, one accumulator per 64 entries, then s (.) + z sum(q) in fp32;
 //   O^T [D, 8 rows] += V^T [D, 16 tokens] P^T [16 tokens, 8 rows].
 // The cache's layout is that of the A operands, so codes go from memory to the instruction with no shuffle: a
 // word is four pairs (entries of a token for K, two tokens of an entry for V). P^T is S^T's
-// fragment transposed within the warp (movmatrix). Every warp keeps its own running maximum, sum and O^T; a
-// block's warps join theirs in shared memory at the end.
+// fragment transposed within the warp (movmatrix). With few rows this is bound by HBM, then by the issue
+// slots of the decoding.
+//
+// Work is split evenly whatever the lengths: the visible blocks of all (sequence, kv head, row tile), in pairs, in a
+// row are cut into equal ranges, one per CTA of a grid that fills the SMs once; every CTA finds its range from
+// the lens itself. A CTA's four warps take the pairs of a range in turn, each through its own ring of bulk
+// copies (a block is contiguous, 18 D bytes) and with its own running maximum, sum and O^T, and join them in
+// shared memory. A (sequence, head, tile) that lies in one range is finished there; the pieces of one that
+// crosses ranges go to the workspace and a second, small kernel joins them, in the order of the ranges.
+// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 86 us (3.8 TB/s), bound
+// by instruction issue (57 % of the slots, 337 warp instructions per block).
 #include <math.h>
+
+#include <mutex>
 
 #include "tern_cache.cuh"
 
@@ -21,8 +32,19 @@ namespace {
 using namespace kv;
 
 constexpr int kWarps = 4;
-constexpr int kRows = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kPair = 2 * kTok;            // tokens of a unit of work: two blocks
+constexpr int kSlots = 3;                  // units in a warp's ring
+constexpr int kSetup = 12;                 // what a (sequence, head, tile) costs beyond its units, in units (measured: its
+                                           // queries, pages and join; 64 sequences of up to 8192 tokens 112.7 us with 0,
+                                           // 102.8 with 4, 90.5 with 8, 86.1 with 12, 87.9 with 24)
+constexpr int kMinUnits = 8;               // cost per CTA at least
 constexpr float kLog2e = 1.4426950408889634f;
+
+struct Desc {               // a (sequence, kv head, row tile) in pieces: where the first lies
+    int b, h, rt, pieces;   // pieces < 2: nothing to join
+    int cta;
+};
 
 struct Args {
     Pool pool;
@@ -30,10 +52,20 @@ struct Args {
     __half* o;
     const int32_t* lens;
     const int32_t* counts;
-    int64_t window, sinks;
-    int B, T, heads, G;         // G = heads per kv head
-    float scale;
+    int window, sinks;
+    int B, T, heads, G, RT;     // G = heads per kv head, RT = row tiles
+    float scale;                // of the exponents (to base 2), > 0
+    float slack;                // 8 / scale
+    uint32_t sign;              // turns the queries' signs where the caller's scale is negative
+    Desc* desc;                 // [ndesc]: by (sequence, head, tile) where these are fewer than the CTAs, else by CTA
+    int ndesc;
+    bool by_segment;
+    float* part;                // [gridDim.x][2 (continued from the range before, or not)][rows][D + 2]
+    unsigned int* status;
 };
+
+template <int D, int NT>
+constexpr int part_floats() { return 8 * NT * (D + 2); }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     uint32_t d;
@@ -55,240 +87,612 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[W]) {
     }
 }
 
-// What a lane knows of its two rows (columns 2 q and 2 q + 1 of the tile): the token each query sits at (-1:
-// no query).
-struct Rows {
-    int64_t pos[2];
-    int64_t first, last;        // of the tile's queries: the smallest and the largest token
+// A sequence's part of the work: its queries' places and the pairs of blocks that they see, as one list (the
+// pairs of the always visible first tokens, then those of the window).
+struct Seq {
+    int cnt, first, last;       // queries; the tokens of the first and the last
+    int blocks;                 // blocks 0 .. blocks - 1 may be read
+    int sb, wb, n;              // pairs 0 .. sb - 1, then wb ..; n in all
+    __device__ __forceinline__ int pair(int v) const { return v < sb ? v : wb + v - sb; }
+    __device__ __forceinline__ int cost() const { return max(n, 1) + kSetup; }   // one unit at least, so that its rows are written
 };
 
-__device__ __forceinline__ bool sees(int64_t pos, int64_t j, int64_t window, int64_t sinks) {
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+    Seq s;
+    const int len = max(0, __ldg(a.lens + b));
+    s.cnt = a.counts ? min(max(__ldg(a.counts + b), 0), a.T) : a.T;
+    s.first = len - s.cnt;
+    s.last = len - 1;
+    s.blocks = s.last < 0 ? 0 : int(min(int64_t(s.last / kTok + 1), a.pool.width * a.pool.per_page));
+    s.sb = s.wb = s.n = 0;
+    if (s.cnt == 0 || s.blocks == 0) return s;
+    const int end = (s.blocks + 1) / 2;
+    if (a.window > 0) {
+        s.wb = min(max(0, s.first - a.window + 1) / kPair, end);
+        s.sb = min(int((unsigned(a.sinks) + kPair - 1) / kPair), s.wb);
+    }
+    s.n = s.sb + end - s.wb;
+    return s;
+}
+
+__device__ __forceinline__ bool sees(int pos, int j, int window, int sinks) {
     return j <= pos && (window <= 0 || j > pos - window || j < sinks);
 }
 
-template <int D>
-struct State {
-    float m[2], l[2];
-    float o[D / 16][4];
-};
-
-template <int D>
-__device__ __forceinline__ void init(State<D>& st) {
-    st.m[0] = st.m[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// One block of 16 tokens, j0 the first. kMask: some row does not see some token.
-template <int D, bool kMask>
-__device__ __forceinline__ void block_step(const uint8_t* unit, int64_t j0, const uint32_t (&qf)[D / 32][4],
-                                           const float (&qsum)[D / kGrp][2], const Rows& rows, const Args& a,
-                                           float scale, State<D>& st) {
-    constexpr int W = D / 32, NG = D / kGrp;
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    uint32_t ka[W], kb[W], va[W], vb[W];
-    load_words(unit + lane * W * 4, ka);
-    load_words(unit + (32 + lane) * W * 4, kb);
-    load_words(unit + v_codes(D) + lane * W * 4, va);
-    load_words(unit + v_codes(D) + (32 + lane) * W * 4, vb);
+template <int D, int NT>
+struct State {
+    float m[NT][2], l[NT][2];   // of rows 2 q and 2 q + 1 of each 8: maximum of q k, sum of this lane's tokens alone
+    float o[NT][D / 16][4];
+};
 
-    float s[4] = {0.f, 0.f, 0.f, 0.f};   // [token g: rows 2q, 2q+1][token g + 8: the same]
+// Pair P of a word's codes plus 64, exactly: codes in bits 4-7 under the exponent of 64 count 1 each; those in bits
+// 0-3 come under that of 1024 and lose 960. What the 64 add to a product is 64 sum(q), taken off with the zero.
+template <int P>
+__device__ __forceinline__ uint32_t code_pair_64(uint32_t w, uint32_t w8) {
+    const uint32_t v = P < 2 ? w : w8;
+    if (P & 1) return lop3_and_or(v, 0x00F000F0u, 0x54005400u);
+    return as_u32(__hsub2(as_h2(lop3_and_or(v, 0x000F000Fu, 0x64006400u)), as_h2(0x63806380u)));
+}
+
+// Two blocks of 16 tokens in shared memory, j0 the first token. kMask: some row does not see some token, or a
+// block is missing (bit i of present: block i is there). The maximum is that of q k.
+template <int D, int NT, bool kMask>
+__device__ __forceinline__ void pair_step(const uint8_t* unit, int j0, unsigned present, const uint32_t (&qf)[NT][D / 32][4],
+                                          const float (&qsum)[NT][D / kGrp][2], const int (&pos)[NT][2],
+                                          const Args& a, State<D, NT>& st) {
+    constexpr int W = D / 32, NG = D / kGrp, U = unit_bytes(D);
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    float s[2][NT][4];                   // [block][8 rows][token g: rows 2q, 2q+1; token g + 8: the same]
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 2 * n; j < 2 * n + 2; ++j) {
-            const uint32_t a8 = ka[j] >> 8, b8 = kb[j] >> 8;
-            const uint32_t A0[4] = {code_pair<0, 0>(ka[j], a8), code_pair<0, 0>(kb[j], b8), code_pair<1, 0>(ka[j], a8),
-                                    code_pair<1, 0>(kb[j], b8)};
-            const uint32_t A1[4] = {code_pair<2, 0>(ka[j], a8), code_pair<2, 0>(kb[j], b8), code_pair<3, 0>(ka[j], a8),
-                                    code_pair<3, 0>(kb[j], b8)};
-            mma_16816(acc, A0, qf[j][0], qf[j][1]);
-            mma_16816(acc, A1, qf[j][2], qf[j][3]);
+    for (int k = 0; k < 2; ++k) {
+        const uint8_t* u = unit + k * U;
+        uint32_t ka[W], kb[W];
+        load_words(u + lane * W * 4, ka);
+        load_words(u + (32 + lane) * W * 4, kb);
+        uint32_t sz[2][NG];              // (step, zero) of tokens g and g + 8
+        if constexpr (NG == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(u + k_scales(D) + g * 8);
+            const uint2 y = *reinterpret_cast<const uint2*>(u + k_scales(D) + (g + 8) * 8);
+            sz[0][0] = x.x, sz[0][1] = x.y, sz[1][0] = y.x, sz[1][1] = y.y;
+        } else {
+            sz[0][0] = *reinterpret_cast<const uint32_t*>(u + k_scales(D) + g * 4);
+            sz[1][0] = *reinterpret_cast<const uint32_t*>(u + k_scales(D) + (g + 8) * 4);
         }
-        const __half2* ks = reinterpret_cast<const __half2*>(unit + k_scales(D));
-        const float2 s0 = __half22float2(ks[g * NG + n]), s1 = __half22float2(ks[(g + 8) * NG + n]);
-        s[0] += s0.x * acc[0] + s0.y * qsum[n][0];
-        s[1] += s0.x * acc[1] + s0.y * qsum[n][1];
-        s[2] += s1.x * acc[2] + s1.y * qsum[n][0];
-        s[3] += s1.x * acc[3] + s1.y * qsum[n][1];
-    }
-    // Steps and zeros of the lane's V tokens 2q, 2q + 1 (index 0) and 2q + 8, 2q + 9 (index 1), per 64 entries.
-    uint32_t vs[NG][2], vz[NG][2];
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-        const uint4 v = *reinterpret_cast<const uint4*>(unit + v_scales(D) + (q * NG + n) * 16);
-        vs[n][0] = v.x, vs[n][1] = v.y, vz[n][0] = v.z, vz[n][1] = v.w;
-    }
+        for (int n = 0; n < NG; ++n) {
+            float acc[NT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] *= scale;
+            for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+            for (int j = 2 * n; j < 2 * n + 2; ++j) {
+                const uint32_t a8 = ka[j] >> 8, b8 = kb[j] >> 8;
+                const uint32_t A0[4] = {code_pair_64<0>(ka[j], a8), code_pair_64<0>(kb[j], b8), code_pair_64<1>(ka[j], a8),
+                                        code_pair_64<1>(kb[j], b8)};
+                const uint32_t A1[4] = {code_pair_64<2>(ka[j], a8), code_pair_64<2>(kb[j], b8), code_pair_64<3>(ka[j], a8),
+                                        code_pair_64<3>(kb[j], b8)};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma_16816(acc[t], A0, qf[t][j][0], qf[t][j][1]);
+                    mma_16816(acc[t], A1, qf[t][j][2], qf[t][j][3]);
+                }
+            }
+            const float2 f0 = __half22float2(as_h2(sz[0][n])), f1 = __half22float2(as_h2(sz[1][n]));
+            const float z0 = f0.y - 64.f * f0.x, z1 = f1.y - 64.f * f1.x;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float rest = (i < 2 ? z0 : z1) * qsum[t][n][i & 1];
+                    s[k][t][i] = (i < 2 ? f0.x : f1.x) * acc[t][i] + (n ? s[k][t][i] + rest : rest);
+                }
+        }
+    }
+    uint32_t keep[2][2];                 // masks of V's scales: [block][tokens 2q, 2q + 1; 2q + 8, 2q + 9]
     if (kMask) {
         // A V token that no row sees, or whose scales are not finite, counts as zeros in the product; a
         // row that sees one of the latter becomes NaN through its sum instead.
-        const __half* vh = reinterpret_cast<const __half*>(unit + v_scales(D));
-        bool odd[2] = {false, false};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int k = 0; k < 2; ++k) {
+            const __half* vh = reinterpret_cast<const __half*>(unit + k * U + v_scales(D));
 #pragma unroll
-            for (int n = 0; n < NG; ++n)
+            for (int h = 0; h < 2; ++h) {
+                bool odd = false, used = false;
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float f = __half2float(vh[((g >> 1) * NG + n) * 8 + z * 4 + 2 * h + (g & 1)]);
-                    odd[h] |= !(fabsf(f) < INFINITY);
-                }
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!sees(rows.pos[i & 1], j0 + g + 8 * (i >> 1), a.window, a.sinks)) s[i] = -INFINITY;
-            else if (odd[i >> 1]) s[i] = NAN;
-        }
-        const bool used0 = s[0] != -INFINITY || s[1] != -INFINITY, used1 = s[2] != -INFINITY || s[3] != -INFINITY;
-        unsigned keep0 = __ballot_sync(0xffffffffu, used0 && !odd[0]), keep1 = __ballot_sync(0xffffffffu, used1 && !odd[1]);
-        // bits 4 t .. 4 t + 3: token t, any of its lanes
+                    for (int z = 0; z < 2; ++z) {
+                        const float f = __half2float(vh[((g >> 1) * NG + n) * 8 + z * 4 + 2 * h + (g & 1)]);
+                        odd |= !(fabsf(f) < INFINITY);
+                    }
+                const int j = j0 + k * kTok + 8 * h + g;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const unsigned keep = h ? keep1 : keep0;
-            const uint32_t mask = ((keep >> (8 * q)) & 0xFu ? 0x0000FFFFu : 0u) | ((keep >> (8 * q + 4)) & 0xFu ? 0xFFFF0000u : 0u);
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                vs[n][h] &= mask;
-                vz[n][h] &= mask;
+                    for (int c = 0; c < 2; ++c) {
+                        if (!(present >> k & 1u) || !sees(pos[t][c], j, a.window, a.sinks)) s[k][t][2 * h + c] = -INFINITY;
+                        else {
+                            used = true;
+                            if (odd) s[k][t][2 * h + c] = NAN;
+                        }
+                    }
+                const unsigned kept = __ballot_sync(0xffffffffu, used && !odd);   // bits 4 t .. 4 t + 3: token t
+                keep[k][h] = ((kept >> (8 * q)) & 0xFu ? 0x0000FFFFu : 0u) | ((kept >> (8 * q + 4)) & 0xFu ? 0xFFFF0000u : 0u);
             }
         }
     }
-    // running maximum of each row: over the lane's two tokens, then over the 8 lanes of its column
-    float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+    // The running maximum of a row moves only when some token is 2^8 above it (a probability may then be up to 2^8,
+    // well inside fp16): seldom, so the reduction over the 8 lanes of a column is not paid per step.
+    bool up = false;
+    float mx[NT][2];
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-    }
-    if (__any_sync(0xffffffffu, mx[0] > st.m[0] || mx[1] > st.m[1])) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const float m = fmaxf(st.m[c], mx[c]);
-            const float f = m > st.m[c] ? exp2f(st.m[c] - m) : 1.f;
-            st.m[c] = m;
-            st.l[c] *= f;
+            mx[t][c] = fmaxf(fmaxf(s[0][t][c], s[0][t][2 + c]), fmaxf(s[1][t][c], s[1][t][2 + c]));
+            up |= mx[t][c] > st.m[t][c] + a.slack;
+        }
+    if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                st.o[i][c] *= f;
-                st.o[i][2 + c] *= f;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float m = fmaxf(mx[t][c], st.m[t][c]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float f = m > st.m[t][c] ? ex2((st.m[t][c] - m) * a.scale) : 1.f;
+                st.m[t][c] = m;
+                st.l[t][c] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    st.o[t][i][c] *= f;
+                    st.o[t][i][2 + c] *= f;
+                }
+            }
+    }
+    float ms[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ms[t][c] = kMask && st.m[t][c] == -INFINITY ? 0.f : st.m[t][c] * a.scale;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint8_t* u = unit + k * U + v_codes(D);
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[k][t][i], a.scale, -ms[t][i & 1]));
+            st.l[t][0] += p[0] + p[2];
+            st.l[t][1] += p[1] + p[3];
+            b0[t] = transposed(pack_h2(p[0], p[1]));
+            b1[t] = transposed(pack_h2(p[2], p[3]));
+        }
+        uint32_t va[W], vb[W];
+        load_words(u + lane * W * 4, va);
+        load_words(u + (32 + lane) * W * 4, vb);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            // steps and zeros of the lane's V tokens 2q, 2q + 1 and 2q + 8, 2q + 9
+            uint4 v = *reinterpret_cast<const uint4*>(unit + k * U + v_scales(D) + (q * NG + n) * 16);
+            if (kMask) {
+                v.x &= keep[k][0], v.z &= keep[k][0];
+                v.y &= keep[k][1], v.w &= keep[k][1];
+            }
+            const __half2 s0 = as_h2(v.x), s1 = as_h2(v.y), z0 = as_h2(v.z), z1 = as_h2(v.w);
+#pragma unroll
+            for (int j = 2 * n; j < 2 * n + 2; ++j) {
+                const uint32_t a8 = va[j] >> 8, b8 = vb[j] >> 8;
+                const uint32_t A0[4] = {as_u32(__hfma2(as_h2(code_pair<0, 0>(va[j], a8)), s0, z0)),
+                                        as_u32(__hfma2(as_h2(code_pair<1, 0>(va[j], a8)), s0, z0)),
+                                        as_u32(__hfma2(as_h2(code_pair<0, 0>(vb[j], b8)), s1, z1)),
+                                        as_u32(__hfma2(as_h2(code_pair<1, 0>(vb[j], b8)), s1, z1))};
+                const uint32_t A1[4] = {as_u32(__hfma2(as_h2(code_pair<2, 0>(va[j], a8)), s0, z0)),
+                                        as_u32(__hfma2(as_h2(code_pair<3, 0>(va[j], a8)), s0, z0)),
+                                        as_u32(__hfma2(as_h2(code_pair<2, 0>(vb[j], b8)), s1, z1)),
+                                        as_u32(__hfma2(as_h2(code_pair<3, 0>(vb[j], b8)), s1, z1))};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma_16816(st.o[t][2 * j], A0, b0[t], b1[t]);
+                    mma_16816(st.o[t][2 * j + 1], A1, b0[t], b1[t]);
+                }
             }
         }
-    }
-    float p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float m = st.m[i & 1];
-        p[i] = exp2f(s[i] - (m == -INFINITY ? 0.f : m));
-    }
-    st.l[0] += p[0] + p[2];
-    st.l[1] += p[1] + p[3];
-    const uint32_t b0 = transposed(pack_h2(p[0], p[1])), b1 = transposed(pack_h2(p[2], p[3]));
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-        const uint32_t a8 = va[j] >> 8, b8 = vb[j] >> 8;
-        const __half2 s0 = as_h2(vs[j / 2][0]), s1 = as_h2(vs[j / 2][1]), z0 = as_h2(vz[j / 2][0]), z1 = as_h2(vz[j / 2][1]);
-        const uint32_t A0[4] = {as_u32(__hfma2(as_h2(code_pair<0, 0>(va[j], a8)), s0, z0)),
-                                as_u32(__hfma2(as_h2(code_pair<1, 0>(va[j], a8)), s0, z0)),
-                                as_u32(__hfma2(as_h2(code_pair<0, 0>(vb[j], b8)), s1, z1)),
-                                as_u32(__hfma2(as_h2(code_pair<1, 0>(vb[j], b8)), s1, z1))};
-        const uint32_t A1[4] = {as_u32(__hfma2(as_h2(code_pair<2, 0>(va[j], a8)), s0, z0)),
-                                as_u32(__hfma2(as_h2(code_pair<3, 0>(va[j], a8)), s0, z0)),
-                                as_u32(__hfma2(as_h2(code_pair<2, 0>(vb[j], b8)), s1, z1)),
-                                as_u32(__hfma2(as_h2(code_pair<3, 0>(vb[j], b8)), s1, z1))};
-        mma_16816(st.o[2 * j], A0, b0, b1);
-        mma_16816(st.o[2 * j + 1], A1, b0, b1);
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const Args a) {
-    constexpr int W = D / 32, NG = D / kGrp;
-    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows], sm_o[kWarps][kRows][D + 1];
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, warp = threadIdx.x >> 5;
-    const int64_t b = blockIdx.z;
-    const int h = blockIdx.y, r0 = blockIdx.x * kRows;
-    const int64_t len = max(0, __ldg(a.lens + b));
-    const int cnt = a.counts ? min(max(__ldg(a.counts + b), 0), a.T) : a.T;
-    if (r0 >= cnt * a.G) return;
-    // row R of the tile: query token R / G, head R % G of the kv head
-    auto q_at = [&](int R) { return ((b * a.T + R / a.G) * a.heads + h * a.G + R % a.G) * D; };
-    auto pos_of = [&](int R) { return R < cnt * a.G ? len - cnt + R / a.G : int64_t(-1); };
+// The lane with `who` announces `expect` bytes on the barrier and starts a bulk copy of `bytes` (0: none).
+__device__ __forceinline__ void bulk_pair(bool who, uint32_t expect, uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p, c;\n\t"
+        "setp.ne.u32 p, %0, 0;\n\t"
+        "setp.ne.and.u32 c, %4, 0, p;\n\t"
+        "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %1;\n\t"
+        "@c cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%2], [%3], %4, [%5];\n\t}" ::"r"(uint32_t(who)),
+        "r"(expect), "r"(to), "l"(reinterpret_cast<uint64_t>(from)), "r"(bytes), "r"(bar)
+        : "memory");
+}
 
-    uint32_t qf[W][4];
-    float part[NG];
-#pragma unroll
-    for (int n = 0; n < NG; ++n) part[n] = 0.f;
-    const bool real = r0 + g < cnt * a.G;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-        const uint4 v = real ? *reinterpret_cast<const uint4*>(a.q + q_at(r0 + g) + 32 * j + 8 * q) : make_uint4(0, 0, 0, 0);
-        qf[j][0] = v.x, qf[j][1] = v.y, qf[j][2] = v.z, qf[j][3] = v.w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(as_h2(qf[j][i]));
-            part[j / 2] += f.x + f.y;
-        }
-    }
-    float qsum[NG][2];
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-        part[n] += __shfl_xor_sync(0xffffffffu, part[n], 1);
-        part[n] += __shfl_xor_sync(0xffffffffu, part[n], 2);
-        qsum[n][0] = __shfl_sync(0xffffffffu, part[n], 8 * q);
-        qsum[n][1] = __shfl_sync(0xffffffffu, part[n], 8 * q + 4);
-    }
-    Rows rows;
-    rows.pos[0] = pos_of(r0 + 2 * q);
-    rows.pos[1] = pos_of(r0 + 2 * q + 1);
-    rows.first = len - cnt + r0 / a.G;
-    rows.last = len - cnt + (min(r0 + kRows, cnt * a.G) - 1) / a.G;
-    const float scale = a.scale * kLog2e;
+// A second copy on a barrier that expects its bytes already.
+__device__ __forceinline__ void bulk_more(bool who, uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %0, 0;\n\t"
+        "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2], %3, [%4];\n\t}" ::"r"(uint32_t(who)),
+        "r"(to), "l"(reinterpret_cast<uint64_t>(from)), "r"(bytes), "r"(bar)
+        : "memory");
+}
 
-    State<D> st;
-    init(st);
-    const int64_t blocks = rows.last < 0 ? 0 : min(rows.last / kTok + 1, a.pool.width * a.pool.per_page);
-    for (int64_t blk = warp; blk < blocks; blk += kWarps) {
-        const int64_t j0 = blk * kTok;
-        if (a.window > 0 && j0 + kTok - 1 <= rows.first - a.window && j0 >= a.sinks) continue;
-        const uint8_t* unit = a.pool.block<D>(b, h, blk);
-        if (!unit) continue;
-        const bool whole = j0 + kTok - 1 <= rows.first && (a.window <= 0 || j0 > rows.last - a.window || j0 + kTok <= a.sinks);
-        if (whole) block_step<D, false>(unit, j0, qf, qsum, rows, a, scale, st);
-        else block_step<D, true>(unit, j0, qf, qsum, rows, a, scale, st);
+// Inclusive sum over the CTA's threads; total: over all of them. `sums` holds kWarps values and is free again
+// after the next barrier.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
     }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
-        st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
-    }
-    if (g == 0) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            sm_m[warp][2 * q + c] = st.m[c];
-            sm_l[warp][2 * q + c] = st.l[c];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sm_o[warp][2 * q + (c & 1)][16 * i + g + 8 * (c >> 1)] = st.o[i][c];
+    if (lane == 31) sums[warp] = v;
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * D; i += kWarps * 32) {
-        const int r = i / D, d = i % D;
-        if (r0 + r >= cnt * a.G) continue;
-        float m = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm_m[w][r]);
-        float l = 0.f, o = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = m == -INFINITY ? 1.f : exp2f(sm_m[w][r] - m);
-            l += f * sm_l[w][r];
-            o += f * sm_o[w][r][d];
-        }
-        a.o[q_at(r0 + r) + d] = __float2half_rn(l == 0.f ? 0.f : o / l);
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) v += sums[w];
+        total += sums[w];
     }
+    __syncthreads();
+    return v;
+}
+
+template <int D, int NT>
+struct Smem {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kPitch = D + 1;
+    static constexpr int ring_bytes = kSlots * 2 * unit_bytes(D);      // of a warp; its O^T after the last unit
+    static_assert(kRows * kPitch * 4 <= ring_bytes, "a warp's rows fit its ring");
+    alignas(128) uint8_t ring[kWarps][ring_bytes];
+    uint64_t full[kWarps][kSlots];
+    int64_t sums[kWarps];
+    int64_t off;
+    int b;
+    float m[kWarps][kRows], l[kWarps][kRows];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(const Args a) {
+    using S = Smem<D, NT>;
+    constexpr int W = D / 32, NG = D / kGrp, kRows = 8 * NT, U = unit_bytes(D);   // U: bytes of a block
+    extern __shared__ __align__(128) uint8_t raw[];
+    S& sm = *reinterpret_cast<S*>(raw);
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kSlots; ++i) mbar_init(&sm.full[0][i], 1);
+        fence_barrier_init();
+    }
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    // ---- this CTA's range of the cost of all (sequence, head, tile)
+    const int per_seq = a.pool.heads * a.RT;
+    int64_t total = 0, mine = 0, incl = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        mine = b < a.B ? int64_t(seq_of(a, b).cost()) * per_seq : 0;
+        int64_t t;
+        incl = total + block_scan(mine, sm.sums, t);
+        total += t;
+    }
+    const int64_t quota = max((total + gridDim.x - 1) / gridDim.x, int64_t(kMinUnits));
+    const int64_t u0 = int64_t(blockIdx.x) * quota;
+    if (u0 >= total) {
+        if (threadIdx.x == 0 && !a.by_segment) a.desc[blockIdx.x].pieces = 0;
+        return;
+    }
+    if (a.B <= kThreads) {
+        if (mine && incl - mine <= u0 && u0 < incl) {
+            sm.b = threadIdx.x;
+            sm.off = u0 - (incl - mine);
+        }
+    } else {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + threadIdx.x;
+            mine = b < a.B ? int64_t(seq_of(a, b).cost()) * per_seq : 0;
+            int64_t t;
+            incl = before + block_scan(mine, sm.sums, t);
+            if (mine && incl - mine <= u0 && u0 < incl) {
+                sm.b = b;
+                sm.off = u0 - (incl - mine);
+            }
+            before += t;
+            if (before > u0) break;
+        }
+    }
+    __syncthreads();
+    int b = sm.b;
+    Seq seq = seq_of(a, b);
+    int ht = int(sm.off / seq.cost());                     // head and tile
+    int c0 = int(sm.off - int64_t(ht) * seq.cost());       // and how much of its cost lies before this range
+    int64_t left = min(quota, total - u0);
+    Desc cut{0, 0, 0, 0, 0};    // the segment that goes on behind this range, if it begins in it
+    const bool odd_page = a.pool.per_page & 1;             // a pair may lie in two pages
+    uint64_t* full = sm.full[warp];
+    uint8_t* ring = sm.ring[warp];
+    const uint32_t ring_at = smem_u32(ring), full_at = smem_u32(full);
+    uint32_t slot = 0, phase = 0;      // of the next unit this warp waits for, over all segments
+    bool ok = true;
+
+    while (left > 0) {
+        const int h = ht / a.RT, r0 = (ht % a.RT) * kRows;
+        const int c1 = int(min(int64_t(seq.cost()), c0 + left));
+        const int v0 = max(0, c0 - kSetup), v1 = max(0, c1 - kSetup);   // units of this range
+        if (v1 > 0) {
+        const int rows = seq.cnt * a.G;                    // of this sequence and head; the tile's are r0 ..
+        const bool live = r0 < rows && seq.n > 0;
+        // ---- the warp's units v0 + warp, + kWarps, ..; lane i looks up the pages of the i-th of each 32: the block's place in
+        // the pool, and two ballots for which of its blocks there are
+        const int n = live ? (v1 - v0 - warp + kWarps - 1) / kWarps : 0;
+        uint32_t at0 = 0, at1 = 0, have0 = 0, have1 = 0;
+        uint32_t present = 0;          // two bits per slot
+        auto look = [&](int i0) {
+            const int blk = 2 * seq.pair(v0 + warp + (i0 + lane) * kWarps);
+            const bool want = i0 + lane < n;
+            const int p0 = want ? a.pool.place(b, h, blk) : -1;
+            const int p1 = !want || blk + 1 >= seq.blocks ? -1 : !odd_page ? p0 : a.pool.place(b, h, blk + 1);
+            at0 = uint32_t(p0), at1 = uint32_t(p1);
+            have0 = __ballot_sync(0xffffffffu, p0 >= 0);
+            have1 = __ballot_sync(0xffffffffu, p1 >= 0);
+        };
+        auto issue = [&](int i, uint32_t slot) {
+            if ((i & 31) == 0) look(i);
+            const unsigned h0 = have0 >> (i & 31) & 1u, h1 = have1 >> (i & 31) & 1u;
+            present = (present & ~(3u << (2 * slot))) | (h0 | h1 << 1) << (2 * slot);
+            const uint32_t p0 = __shfl_sync(0xffffffffu, at0, i & 31);
+            const uint32_t to = ring_at + slot * 2 * U, bar = full_at + slot * 8;
+            const uint32_t bytes = (h0 + h1) * U;
+            if (!odd_page) {
+                bulk_pair(lane == 0, bytes, to, a.pool.pool + uint64_t(p0) * U, bytes, bar);
+            } else {
+                const uint32_t p1 = __shfl_sync(0xffffffffu, at1, i & 31);
+                bulk_pair(lane == 0, bytes, to, a.pool.pool + uint64_t(p0) * U, h0 * U, bar);
+                bulk_more(lane == 0 && h1, to + U, a.pool.pool + uint64_t(p1) * U, U, bar);
+            }
+        };
+        int issued = 0;
+        for (uint32_t at = slot; issued < n && issued < kSlots; ++issued) {
+            issue(issued, at);
+            at = at == kSlots - 1 ? 0 : at + 1;
+        }
+
+        // ---- the tile's queries: row R is token R / G, head R % G of the kv head
+        auto row_at = [&](int R) { return ((int64_t(b) * a.T + R / a.G) * a.heads + h * a.G + R % a.G) * D; };
+        uint32_t qf[NT][W][4];
+        float qsum[NT][NG][2];
+        int pos[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float part[NG];
+#pragma unroll
+            for (int i = 0; i < NG; ++i) part[i] = 0.f;
+            const int R = r0 + 8 * t + g;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const uint4 v = R < rows && n > 0 ? *reinterpret_cast<const uint4*>(a.q + row_at(R) + 32 * j + 8 * q) : make_uint4(0, 0, 0, 0);
+                qf[t][j][0] = v.x ^ a.sign, qf[t][j][1] = v.y ^ a.sign, qf[t][j][2] = v.z ^ a.sign, qf[t][j][3] = v.w ^ a.sign;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __half22float2(as_h2(qf[t][j][i]));
+                    part[j / 2] += f.x + f.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
+                part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
+                qsum[t][i][0] = __shfl_sync(0xffffffffu, part[i], 8 * q);
+                qsum[t][i][1] = __shfl_sync(0xffffffffu, part[i], 8 * q + 4);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int Rc = r0 + 8 * t + 2 * q + c;
+                pos[t][c] = Rc < rows ? seq.first + Rc / a.G : -1;
+            }
+        }
+        const int tile_first = seq.first + r0 / a.G, tile_last = seq.first + (min(r0 + kRows, rows) - 1) / a.G;
+        State<D, NT> st;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            st.m[t][0] = st.m[t][1] = -INFINITY;
+            st.l[t][0] = st.l[t][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) st.o[t][i][0] = st.o[t][i][1] = st.o[t][i][2] = st.o[t][i][3] = 0.f;
+        }
+        // units [whole0, whole1) and [0, sink1) of the list: every row sees every token
+        const int whole1 = seq.sb + max(0, (tile_first + 1) / kPair - seq.wb);
+        const int whole0 = a.window > 0 ? seq.sb + max(0, max(0, tile_last - a.window + kPair) / kPair - seq.wb) : 0;
+        const int sink1 = a.window > 0 ? min(seq.sb, min(a.sinks, tile_first + 1) / kPair) : 0;
+        for (int i = 0; i < n; ++i) {
+            if (!mbar_wait(&full[slot], phase)) ok = false;
+            const int v = v0 + warp + i * kWarps;
+            const unsigned have = present >> (2 * slot) & 3u;
+            const bool whole = have == 3u && ((v >= whole0 && v < whole1) || v < sink1);
+            const uint8_t* unit = ring + slot * 2 * U;
+            if (whole) pair_step<D, NT, false>(unit, 0, 3u, qf, qsum, pos, a, st);
+            else if (have) pair_step<D, NT, true>(unit, seq.pair(v) * kPair, have, qf, qsum, pos, a, st);
+            __syncwarp();       // every lane has read the slot: the unit kSlots further on goes there
+            if (issued < n) issue(issued++, slot);
+            if (++slot == kSlots) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+        // ---- join the warps
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = st.l[t][c];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                if (g == 0) {
+                    sm.m[warp][8 * t + 2 * q + c] = st.m[t][c];
+                    sm.l[warp][8 * t + 2 * q + c] = l;
+                }
+            }
+        float* wo = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    wo[(8 * t + 2 * q + (c & 1)) * S::kPitch + 16 * i + g + 8 * (c >> 1)] = st.o[t][i][c];
+        __syncthreads();
+        const bool begins = v0 == 0, ends = c1 == seq.cost();
+        if (begins) {
+            // its other pieces are the next ranges' first ones
+            const int pieces = ends ? 1 : 1 + int((seq.cost() - c1 + quota - 1) / quota);
+            cut = Desc{b, h, ht % a.RT, pieces, int(blockIdx.x)};
+            if (a.by_segment && threadIdx.x == 0) a.desc[b * per_seq + ht] = cut;
+        }
+        float* part = a.part + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * part_floats<D, NT>();
+        for (int i = threadIdx.x; i < kRows * D; i += kThreads) {
+            const int r = i / D, d = i % D;
+            if (r0 + r >= rows) break;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][r]);
+            float l = 0.f, o = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = m == -INFINITY ? 1.f : exp2f((sm.m[w][r] - m) * a.scale);
+                l += f * sm.l[w][r];
+                o += f * reinterpret_cast<const float*>(sm.ring[w])[r * S::kPitch + d];
+            }
+            if (begins && ends) {
+                a.o[row_at(r0 + r) + d] = __float2half_rn(l == 0.f ? 0.f : o / l);
+            } else {
+                part[r * (D + 2) + d] = o;
+                if (d == 0) {
+                    part[r * (D + 2) + D] = m * a.scale;
+                    part[r * (D + 2) + D + 1] = l;
+                }
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings' next copies follow these accesses
+        __syncthreads();
+        }
+        left -= c1 - c0;
+        c0 = 0;
+        if (++ht == per_seq && left > 0) {
+            ht = 0;
+            seq = seq_of(a, ++b);
+        }
+    }
+    if (!a.by_segment && threadIdx.x == 0) a.desc[blockIdx.x] = cut;     // of the last segment begun: the only one that can go on
+    if (!ok && a.status) atomicOr(a.status, kStatusTimeout);
+}
+
+// Joins the pieces of the (sequence, head, tile)s that ranges cut: a CTA per row of one, kJoin / D pieces at a time.
+constexpr int kJoin = 256;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
+    constexpr int kRows = 8 * NT, stride = D + 2, kPar = kJoin / D;
+    __shared__ float red[2][kJoin / 32], sum[kPar][D];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const Desc ds = a.desc[blockIdx.x];
+    if (ds.pieces < 2) return;
+    const int r = blockIdx.y, R = ds.rt * kRows + r, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (R >= seq_of(a, ds.b).cnt * a.G) return;
+    // piece 0 begins the segment in its CTA's range; the others continue it in the CTAs after
+    const int64_t size = part_floats<D, NT>();
+    const float* base = a.part + int64_t(ds.cta) * 2 * size + r * stride;
+    auto piece = [&](int p) { return base + (p == 0 ? size : 2 * size * p); };
+    float m = -INFINITY, l = 0.f;
+    for (int p = threadIdx.x; p < ds.pieces; p += kJoin) m = fmaxf(m, piece(p)[D]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoin / 32; ++w) m = fmaxf(m, red[0][w]);
+    const float top = m == -INFINITY ? 0.f : m;
+    for (int p = threadIdx.x; p < ds.pieces; p += kJoin) l += exp2f(piece(p)[D] - top) * piece(p)[D + 1];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) red[1][warp] = l;
+    const int d = threadIdx.x % D, part = threadIdx.x / D;
+    float o = 0.f;
+#pragma unroll 8
+    for (int p = part; p < ds.pieces; p += kPar) o += exp2f(piece(p)[D] - top) * piece(p)[d];
+    sum[part][d] = o;
+    __syncthreads();
+    if (part) return;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoin / 32; ++w) l += red[1][w];
+#pragma unroll
+    for (int i = 1; i < kPar; ++i) o += sum[i][d];
+    a.o[((int64_t(ds.b) * a.T + R / a.G) * a.heads + ds.h * a.G + R % a.G) * D + d] = __float2half_rn(l == 0.f ? 0.f : o / l);
+}
+
+// Rows per tile: 8, or 16 where a kv head has more (the cache is then read half as often).
+int tiles_of(int64_t T, int64_t G) { return T * G > 8 ? 2 : 1; }
+int ctas_of(int nt) { return sm_count() * (nt == 1 ? 4 : 3); }
+
+size_t workspace_of(const tern_cache* c, int64_t T, int64_t heads) {
+    const int nt = tiles_of(T, heads / c->kv_heads);
+    const size_t n = size_t(ctas_of(nt));
+    const size_t desc = (n * sizeof(Desc) + 255) & ~size_t(255);
+    return (desc + n * 2 * size_t(8 * nt * (c->head_dim + 2)) * 4 + 255) & ~size_t(255);
+}
+
+template <int D, int NT>
+tern_status launch(Args& a, void* workspace, cudaStream_t stream) {
+    using S = Smem<D, NT>;
+    static std::mutex mu;
+    static bool configured[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TERN_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!configured[dev]) {
+            if (cudaFuncSetAttribute(attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(S))) != cudaSuccess)
+                return TERN_ERR_CUDA;
+            configured[dev] = true;
+        }
+    }
+    const int n = ctas_of(NT);
+    a.RT = (a.T * a.G + 8 * NT - 1) / (8 * NT);
+    a.desc = static_cast<Desc*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ((size_t(n) * sizeof(Desc) + 255) & ~size_t(255)));
+    a.status = async_status_word();
+    const int64_t segments = int64_t(a.B) * a.pool.heads * a.RT;
+    a.by_segment = segments <= n;
+    a.ndesc = a.by_segment ? int(segments) : n;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(n), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = sizeof(S);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, attention_kernel<D, NT>, a) != cudaSuccess) return TERN_ERR_CUDA;
+    cfg.gridDim = dim3(unsigned(a.ndesc), unsigned(a.T * a.G < 8 * NT ? a.T * a.G : 8 * NT), 1);
+    cfg.blockDim = dim3(kJoin, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
 tern_status check_attention(const tern_cache* c, int64_t B, int64_t T, int64_t heads) {
@@ -305,7 +709,8 @@ using namespace tern;
 using namespace tern::kv;
 
 extern "C" size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, int64_t T, int64_t heads) {
-    return 0;
+    if (check_attention(cache, B, T, heads) != TERN_OK || B == 0 || T == 0) return 0;
+    return workspace_of(cache, T, heads);
 }
 
 extern "C" tern_status tern_cache_attention(const tern_cache* cache, const tern_half* q, int64_t B, int64_t T,
@@ -323,10 +728,23 @@ extern "C" tern_status tern_cache_attention(const tern_cache* cache, const tern_
     const size_t need = tern_cache_attention_workspace_bytes(cache, B, T, heads);
     if (need && (!workspace || workspace_bytes < need)) return TERN_ERR_WORKSPACE;
     if (workspace && !aligned16(workspace)) return TERN_ERR_ALIGN;
-    Args a{pool_of(cache, table, width), reinterpret_cast<const __half*>(q), reinterpret_cast<__half*>(o), lens, counts,
-           window, sinks, int(B), int(T), int(heads), int(heads / cache->kv_heads), scale};
-    const dim3 grid(unsigned((T * a.G + kRows - 1) / kRows), unsigned(cache->kv_heads), unsigned(B));
-    auto kernel = cache->head_dim == 64 ? attention_kernel<64> : attention_kernel<128>;
-    kernel<<<grid, kWarps * 32, 0, as_cuda(stream)>>>(a);
-    return launched();
+    Args a{};
+    a.pool = pool_of(cache, table, width);
+    a.q = reinterpret_cast<const __half*>(q);
+    a.o = reinterpret_cast<__half*>(o);
+    a.lens = lens;
+    a.counts = counts;
+    a.window = int(window < 0x7fffffff ? window : 0x7fffffff);
+    a.sinks = int(sinks < 0x7fffffff ? sinks : 0x7fffffff);
+    a.B = int(B);
+    a.T = int(T);
+    a.heads = int(heads);
+    a.G = int(heads / cache->kv_heads);
+    a.scale = fmaxf(fabsf(scale) * kLog2e, 1e-30f);    // zero is as good as 1e-30
+    a.slack = 8.f / a.scale;
+    a.sign = scale < 0.f ? 0x80008000u : 0u;
+    cudaStream_t cs = as_cuda(stream);
+    if (tiles_of(T, a.G) == 1)
+        return cache->head_dim == 64 ? launch<64, 1>(a, workspace, cs) : launch<128, 1>(a, workspace, cs);
+    return cache->head_dim == 64 ? launch<64, 2>(a, workspace, cs) : launch<128, 2>(a, workspace, cs);
 }
