@@ -27,7 +27,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtern.so")
 LIB_DEBUG = os.path.join(PKG, "libtern_debug.so")
 SOURCES = ["tern_api.cu", "tern_pack.cu", "tern_elem.cu", "tern_gemv.cu", "tern_decode1.cu", "tern_decodem.cu", "tern_gemm_sm100.cu",
-           "tern_rotate.cu", "tern_fit.cu", "tern_nib.cu", "tern_nib_linear.cu", "tern_cache.cu", "tern_cache_attention.cu",
+           "tern_rotate.cu", "tern_fit.cu", "tern_nib.cu", "tern_nib_linear.cu", "tern_nib_gemm.cu", "tern_cache.cu", "tern_cache_attention.cu",
            "tern_bits.cpp"]
 HEADERS = ["tern_internal.cuh", "tern_device.cuh", "tern_stream.cuh", "tern_nib.cuh", "tern_cache.cuh", os.path.join("..", "..", "include", "tern.h")]
 

@@ -34,7 +34,7 @@ using namespace kv;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2 * kTok;            // tokens of a unit of work: two blocks
-constexpr int kSlots = 3;                  // units in a warp's ring
+constexpr int kSlots = 2;                  // units in a warp's ring
 constexpr int kSetup = 12;                 // what a (sequence, head, tile) costs beyond its units, in units (measured: its
                                            // queries, pages and join; 64 sequences of up to 8192 tokens 112.7 us with 0,
                                            // 102.8 with 4, 90.5 with 8, 86.1 with 12, 87.9 with 24)
@@ -43,7 +43,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Desc {               // a (sequence, kv head, row tile) in pieces: where the first lies
     int b, h, rt, pieces;   // pieces < 2: nothing to join
-    int cta;
+    int cta, rows;          // rows of (b, h) that are written
 };
 
 struct Args {
@@ -69,7 +69,7 @@ constexpr int part_floats() { return 8 * NT * (D + 2); }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
 
@@ -131,44 +131,32 @@ struct State {
     float o[NT][D / 16][4];
 };
 
-// Pair P of a word's codes plus 64, exactly: codes in bits 4-7 under the exponent of 64 count 1 each; those in bits
-// 0-3 come under that of 1024 and lose 960. What the 64 add to a product is 64 sum(q), taken off with the zero.
-template <int P>
-__device__ __forceinline__ uint32_t code_pair_64(uint32_t w, uint32_t w8) {
-    const uint32_t v = P < 2 ? w : w8;
-    if (P & 1) return lop3_and_or(v, 0x00F000F0u, 0x54005400u);
-    return as_u32(__hsub2(as_h2(lop3_and_or(v, 0x000F000Fu, 0x64006400u)), as_h2(0x63806380u)));
-}
-
-// Two blocks of 16 tokens in shared memory, j0 the first token. kMask: some row does not see some token, or a
-// block is missing (bit i of present: block i is there). The maximum is that of q k.
+// One block of 16 tokens in shared memory, j0 the first token. kMask: some row does not see some token. The maximum
+// is that of q k.
 template <int D, int NT, bool kMask>
-__device__ __forceinline__ void pair_step(const uint8_t* unit, int j0, unsigned present, const uint32_t (&qf)[NT][D / 32][4],
-                                          const float (&qsum)[NT][D / kGrp][2], const int (&pos)[NT][2],
-                                          const Args& a, State<D, NT>& st) {
-    constexpr int W = D / 32, NG = D / kGrp, U = unit_bytes(D);
+__device__ __forceinline__ void block_step(const uint8_t* u, int j0, const uint32_t (&qf)[NT][D / 32][4],
+                                           const float (&qx)[NT][2], const int (&pos)[NT][2], const Args& a,
+                                           State<D, NT>& st) {
+    constexpr int W = D / 32, NG = D / kGrp;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    float s[2][NT][4];                   // [block][8 rows][token g: rows 2q, 2q+1; token g + 8: the same]
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint8_t* u = unit + k * U;
+    float s[NT][4];                      // [8 rows][token g: rows 2q, 2q+1; token g + 8: the same]
+    {
         uint32_t ka[W], kb[W];
         load_words(u + lane * W * 4, ka);
         load_words(u + (32 + lane) * W * 4, kb);
-        uint32_t sz[2][NG];              // (step, zero) of tokens g and g + 8
-        if constexpr (NG == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(u + k_scales(D) + g * 8);
-            const uint2 y = *reinterpret_cast<const uint2*>(u + k_scales(D) + (g + 8) * 8);
-            sz[0][0] = x.x, sz[0][1] = x.y, sz[1][0] = y.x, sz[1][1] = y.y;
-        } else {
-            sz[0][0] = *reinterpret_cast<const uint32_t*>(u + k_scales(D) + g * 4);
-            sz[1][0] = *reinterpret_cast<const uint32_t*>(u + k_scales(D) + (g + 8) * 4);
+        // What is not s c q of the scores, z sum(q) - 64 s sum(q): a product in tf32, where s and z are exact. Its column q is
+        // half q of the token's scales (s, z per 64 entries), against sum(q)'s upper part, column q + 4 against its lower.
+        float a0 = 0.f, a1 = 0.f;
+        const __half* ks = reinterpret_cast<const __half*>(u + k_scales(D));
+        if (NG == 2 || q < 2) {
+            a0 = __half2float(ks[g * 2 * NG + q]);
+            a1 = __half2float(ks[(g + 8) * 2 * NG + q]);
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_1688_first(s[t], a0, a1, a0, a1, qx[t][0], qx[t][1]);
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             float acc[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
 #pragma unroll
             for (int j = 2 * n; j < 2 * n + 2; ++j) {
                 const uint32_t a8 = ka[j] >> 8, b8 = kb[j] >> 8;
@@ -178,71 +166,60 @@ __device__ __forceinline__ void pair_step(const uint8_t* unit, int j0, unsigned 
                                         code_pair_64<3>(kb[j], b8)};
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    mma_16816(acc[t], A0, qf[t][j][0], qf[t][j][1]);
-                    mma_16816(acc[t], A1, qf[t][j][2], qf[t][j][3]);
+                    if (j == 2 * n) mma_first(acc[t], A0, qf[t][j][0], qf[t][j][1]);
+                    else mma_next(acc[t], A0, qf[t][j][0], qf[t][j][1]);
+                    mma_next(acc[t], A1, qf[t][j][2], qf[t][j][3]);
                 }
             }
-            const float2 f0 = __half22float2(as_h2(sz[0][n])), f1 = __half22float2(as_h2(sz[1][n]));
-            const float z0 = f0.y - 64.f * f0.x, z1 = f1.y - 64.f * f1.x;
+            const float s0 = __half2float(ks[(g * NG + n) * 2]), s1 = __half2float(ks[((g + 8) * NG + n) * 2]);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float rest = (i < 2 ? z0 : z1) * qsum[t][n][i & 1];
-                    s[k][t][i] = (i < 2 ? f0.x : f1.x) * acc[t][i] + (n ? s[k][t][i] + rest : rest);
-                }
+                for (int i = 0; i < 4; ++i) s[t][i] += (i < 2 ? s0 : s1) * acc[t][i];
         }
     }
-    uint32_t keep[2][2];                 // masks of V's scales: [block][tokens 2q, 2q + 1; 2q + 8, 2q + 9]
+    uint32_t keep[2];                    // masks of V's scales: tokens 2q, 2q + 1; 2q + 8, 2q + 9
     if (kMask) {
         // A V token that no row sees, or whose scales are not finite, counts as zeros in the product; a
         // row that sees one of the latter becomes NaN through its sum instead.
+        const __half* vh = reinterpret_cast<const __half*>(u + v_scales(D));
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const __half* vh = reinterpret_cast<const __half*>(unit + k * U + v_scales(D));
+        for (int h = 0; h < 2; ++h) {
+            bool odd = false, used = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                bool odd = false, used = false;
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
+                for (int z = 0; z < 2; ++z) {
+                    const float f = __half2float(vh[((g >> 1) * NG + n) * 8 + z * 4 + 2 * h + (g & 1)]);
+                    odd |= !(fabsf(f) < INFINITY);
+                }
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const float f = __half2float(vh[((g >> 1) * NG + n) * 8 + z * 4 + 2 * h + (g & 1)]);
-                        odd |= !(fabsf(f) < INFINITY);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (!sees(pos[t][c], j0 + 8 * h + g, a.window, a.sinks)) s[t][2 * h + c] = -INFINITY;
+                    else {
+                        used = true;
+                        if (odd) s[t][2 * h + c] = NAN;
                     }
-                const int j = j0 + k * kTok + 8 * h + g;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (!(present >> k & 1u) || !sees(pos[t][c], j, a.window, a.sinks)) s[k][t][2 * h + c] = -INFINITY;
-                        else {
-                            used = true;
-                            if (odd) s[k][t][2 * h + c] = NAN;
-                        }
-                    }
-                const unsigned kept = __ballot_sync(0xffffffffu, used && !odd);   // bits 4 t .. 4 t + 3: token t
-                keep[k][h] = ((kept >> (8 * q)) & 0xFu ? 0x0000FFFFu : 0u) | ((kept >> (8 * q + 4)) & 0xFu ? 0xFFFF0000u : 0u);
-            }
+                }
+            const unsigned kept = __ballot_sync(0xffffffffu, used && !odd);   // bits 4 t .. 4 t + 3: token t
+            keep[h] = ((kept >> (8 * q)) & 0xFu ? 0x0000FFFFu : 0u) | ((kept >> (8 * q + 4)) & 0xFu ? 0xFFFF0000u : 0u);
         }
     }
     // The running maximum of a row moves only when some token is 2^8 above it (a probability may then be up to 2^8,
-    // well inside fp16): seldom, so the reduction over the 8 lanes of a column is not paid per step.
+    // well inside fp16): seldom, so the reduction over the 8 lanes of a column is not paid per block.
     bool up = false;
-    float mx[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            mx[t][c] = fmaxf(fmaxf(s[0][t][c], s[0][t][2 + c]), fmaxf(s[1][t][c], s[1][t][2 + c]));
-            up |= mx[t][c] > st.m[t][c] + a.slack;
-        }
+        for (int c = 0; c < 2; ++c) up |= fmaxf(s[t][c], s[t][2 + c]) > st.m[t][c] + a.slack;
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float m = fmaxf(mx[t][c], st.m[t][c]);
+                float m = fmaxf(fmaxf(s[t][c], s[t][2 + c]), st.m[t][c]);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float f = m > st.m[t][c] ? ex2((st.m[t][c] - m) * a.scale) : 1.f;
@@ -255,53 +232,47 @@ __device__ __forceinline__ void pair_step(const uint8_t* unit, int j0, unsigned 
                 }
             }
     }
-    float ms[NT][2];
+    uint32_t b0[NT], b1[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+        float p[4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) ms[t][c] = kMask && st.m[t][c] == -INFINITY ? 0.f : st.m[t][c] * a.scale;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint8_t* u = unit + k * U + v_codes(D);
-        uint32_t b0[NT], b1[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[k][t][i], a.scale, -ms[t][i & 1]));
-            st.l[t][0] += p[0] + p[2];
-            st.l[t][1] += p[1] + p[3];
-            b0[t] = transposed(pack_h2(p[0], p[1]));
-            b1[t] = transposed(pack_h2(p[2], p[3]));
+        for (int i = 0; i < 4; ++i) {
+            const float ms = kMask && st.m[t][i & 1] == -INFINITY ? 0.f : st.m[t][i & 1] * a.scale;
+            p[i] = ex2(fmaf(s[t][i], a.scale, -ms));
         }
-        uint32_t va[W], vb[W];
-        load_words(u + lane * W * 4, va);
-        load_words(u + (32 + lane) * W * 4, vb);
+        st.l[t][0] += p[0] + p[2];
+        st.l[t][1] += p[1] + p[3];
+        b0[t] = transposed(pack_h2(p[0], p[1]));
+        b1[t] = transposed(pack_h2(p[2], p[3]));
+    }
+    uint32_t va[W], vb[W];
+    load_words(u + v_codes(D) + lane * W * 4, va);
+    load_words(u + v_codes(D) + (32 + lane) * W * 4, vb);
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            // steps and zeros of the lane's V tokens 2q, 2q + 1 and 2q + 8, 2q + 9
-            uint4 v = *reinterpret_cast<const uint4*>(unit + k * U + v_scales(D) + (q * NG + n) * 16);
-            if (kMask) {
-                v.x &= keep[k][0], v.z &= keep[k][0];
-                v.y &= keep[k][1], v.w &= keep[k][1];
-            }
-            const __half2 s0 = as_h2(v.x), s1 = as_h2(v.y), z0 = as_h2(v.z), z1 = as_h2(v.w);
+    for (int n = 0; n < NG; ++n) {
+        // steps and zeros of the lane's V tokens 2q, 2q + 1 and 2q + 8, 2q + 9
+        uint4 v = *reinterpret_cast<const uint4*>(u + v_scales(D) + (q * NG + n) * 16);
+        if (kMask) {
+            v.x &= keep[0], v.z &= keep[0];
+            v.y &= keep[1], v.w &= keep[1];
+        }
+        const __half2 s0 = as_h2(v.x), s1 = as_h2(v.y), z0 = as_h2(v.z), z1 = as_h2(v.w);
 #pragma unroll
-            for (int j = 2 * n; j < 2 * n + 2; ++j) {
-                const uint32_t a8 = va[j] >> 8, b8 = vb[j] >> 8;
-                const uint32_t A0[4] = {as_u32(__hfma2(as_h2(code_pair<0, 0>(va[j], a8)), s0, z0)),
-                                        as_u32(__hfma2(as_h2(code_pair<1, 0>(va[j], a8)), s0, z0)),
-                                        as_u32(__hfma2(as_h2(code_pair<0, 0>(vb[j], b8)), s1, z1)),
-                                        as_u32(__hfma2(as_h2(code_pair<1, 0>(vb[j], b8)), s1, z1))};
-                const uint32_t A1[4] = {as_u32(__hfma2(as_h2(code_pair<2, 0>(va[j], a8)), s0, z0)),
-                                        as_u32(__hfma2(as_h2(code_pair<3, 0>(va[j], a8)), s0, z0)),
-                                        as_u32(__hfma2(as_h2(code_pair<2, 0>(vb[j], b8)), s1, z1)),
-                                        as_u32(__hfma2(as_h2(code_pair<3, 0>(vb[j], b8)), s1, z1))};
+        for (int j = 2 * n; j < 2 * n + 2; ++j) {
+            const uint32_t a8 = va[j] >> 8, b8 = vb[j] >> 8;
+            const uint32_t A0[4] = {as_u32(__hfma2(as_h2(code_pair<0, 0>(va[j], a8)), s0, z0)),
+                                    as_u32(__hfma2(as_h2(code_pair<1, 0>(va[j], a8)), s0, z0)),
+                                    as_u32(__hfma2(as_h2(code_pair<0, 0>(vb[j], b8)), s1, z1)),
+                                    as_u32(__hfma2(as_h2(code_pair<1, 0>(vb[j], b8)), s1, z1))};
+            const uint32_t A1[4] = {as_u32(__hfma2(as_h2(code_pair<2, 0>(va[j], a8)), s0, z0)),
+                                    as_u32(__hfma2(as_h2(code_pair<3, 0>(va[j], a8)), s0, z0)),
+                                    as_u32(__hfma2(as_h2(code_pair<2, 0>(vb[j], b8)), s1, z1)),
+                                    as_u32(__hfma2(as_h2(code_pair<3, 0>(vb[j], b8)), s1, z1))};
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma_16816(st.o[t][2 * j], A0, b0[t], b1[t]);
-                    mma_16816(st.o[t][2 * j + 1], A1, b0[t], b1[t]);
-                }
+            for (int t = 0; t < NT; ++t) {
+                mma_next(st.o[t][2 * j], A0, b0[t], b1[t]);
+                mma_next(st.o[t][2 * j + 1], A1, b0[t], b1[t]);
             }
         }
     }
@@ -420,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
     int ht = int(sm.off / seq.cost());                     // head and tile
     int c0 = int(sm.off - int64_t(ht) * seq.cost());       // and how much of its cost lies before this range
     int64_t left = min(quota, total - u0);
-    Desc cut{0, 0, 0, 0, 0};    // the segment that goes on behind this range, if it begins in it
+    Desc cut{0, 0, 0, 0, 0, 0};    // the segment that goes on behind this range, if it begins in it
     const bool odd_page = a.pool.per_page & 1;             // a pair may lie in two pages
     uint64_t* full = sm.full[warp];
     uint8_t* ring = sm.ring[warp];
@@ -465,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
             }
         };
         int issued = 0;
-        for (uint32_t at = slot; issued < n && issued < kSlots; ++issued) {
+        for (uint32_t at = slot; issued < n && issued < kSlots && ok; ++issued) {
             issue(issued, at);
             at = at == kSlots - 1 ? 0 : at + 1;
         }
@@ -473,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
         // ---- the tile's queries: row R is token R / G, head R % G of the kv head
         auto row_at = [&](int R) { return ((int64_t(b) * a.T + R / a.G) * a.heads + h * a.G + R % a.G) * D; };
         uint32_t qf[NT][W][4];
-        float qsum[NT][NG][2];
+        float qx[NT][2];
         int pos[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -495,9 +466,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
             for (int i = 0; i < NG; ++i) {
                 part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
                 part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
-                qsum[t][i][0] = __shfl_sync(0xffffffffu, part[i], 8 * q);
-                qsum[t][i][1] = __shfl_sync(0xffffffffu, part[i], 8 * q + 4);
             }
+            // of row g: -64 sum(q) against the steps (even columns), sum(q) against the zeros
+            const float mine = NG == 2 && q >= 2 ? part[NG - 1] : part[0];
+            const float v = NG == 2 || q < 2 ? (q & 1 ? mine : -64.f * mine) : 0.f;
+            qx[t][0] = tf32_part(v);
+            qx[t][1] = tf32_part(v - qx[t][0]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int Rc = r0 + 8 * t + 2 * q + c;
@@ -518,15 +492,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
         const int whole0 = a.window > 0 ? seq.sb + max(0, max(0, tile_last - a.window + kPair) / kPair - seq.wb) : 0;
         const int sink1 = a.window > 0 ? min(seq.sb, min(a.sinks, tile_first + 1) / kPair) : 0;
         for (int i = 0; i < n; ++i) {
-            if (!mbar_wait(&full[slot], phase)) ok = false;
+            ok = ok && mbar_wait(&full[slot], phase);
             const int v = v0 + warp + i * kWarps;
             const unsigned have = present >> (2 * slot) & 3u;
             const bool whole = have == 3u && ((v >= whole0 && v < whole1) || v < sink1);
             const uint8_t* unit = ring + slot * 2 * U;
-            if (whole) pair_step<D, NT, false>(unit, 0, 3u, qf, qsum, pos, a, st);
-            else if (have) pair_step<D, NT, true>(unit, seq.pair(v) * kPair, have, qf, qsum, pos, a, st);
+            if (whole) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) block_step<D, NT, false>(unit + k * U, 0, qf, qx, pos, a, st);
+            } else {
+                const int j0 = seq.pair(v) * kPair;
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k)
+                    if (have >> k & 1u) block_step<D, NT, true>(unit + k * U, j0 + k * kTok, qf, qx, pos, a, st);
+            }
             __syncwarp();       // every lane has read the slot: the unit kSlots further on goes there
-            if (issued < n) issue(issued++, slot);
+            if (issued < n && ok) issue(issued++, slot);
             if (++slot == kSlots) {
                 slot = 0;
                 phase ^= 1u;
@@ -558,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
         if (begins) {
             // its other pieces are the next ranges' first ones
             const int pieces = ends ? 1 : 1 + int((seq.cost() - c1 + quota - 1) / quota);
-            cut = Desc{b, h, ht % a.RT, pieces, int(blockIdx.x)};
+            cut = Desc{b, h, ht % a.RT, pieces, int(blockIdx.x), rows};
             if (a.by_segment && threadIdx.x == 0) a.desc[b * per_seq + ht] = cut;
         }
         float* part = a.part + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * part_floats<D, NT>();
@@ -596,51 +577,74 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
         }
     }
     if (!a.by_segment && threadIdx.x == 0) a.desc[blockIdx.x] = cut;     // of the last segment begun: the only one that can go on
-    if (!ok && a.status) atomicOr(a.status, kStatusTimeout);
+    if (!ok) {
+        // a wait ran out: give the copies under way their time to land before the CTA ends
+        for (int i = 0; i < kSlots; ++i) mbar_wait_for(&full[i], phase ^ (i < int(slot)), kWaitLimitCycles / 16);
+        if (a.status) atomicOr(a.status, kStatusTimeout);
+    }
 }
 
-// Joins the pieces of the (sequence, head, tile)s that ranges cut: a CTA per row of one, kJoin / D pieces at a time.
-constexpr int kJoin = 256;
+// Joins the pieces of the (sequence, head, tile)s that ranges cut: a CTA per row of one, kJoin / D pieces at a time, each thread
+// with a running maximum of its own, so that all it needs of four pieces is loaded at once.
+constexpr int kJoin = 512;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
-    constexpr int kRows = 8 * NT, stride = D + 2, kPar = kJoin / D;
-    __shared__ float red[2][kJoin / 32], sum[kPar][D];
+    constexpr int kRows = 8 * NT, stride = D + 2, kPar = kJoin / D, kBatch = 4;
+    __shared__ float sm_m[kPar], sm_l[kPar], sm_o[kPar][D];
     grid_launch_dependents();
     grid_dependency_wait();
     const Desc ds = a.desc[blockIdx.x];
-    if (ds.pieces < 2) return;
-    const int r = blockIdx.y, R = ds.rt * kRows + r, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (R >= seq_of(a, ds.b).cnt * a.G) return;
+    const int r = blockIdx.y, R = ds.rt * kRows + r;
+    if (ds.pieces < 2 || R >= ds.rows) return;
     // piece 0 begins the segment in its CTA's range; the others continue it in the CTAs after
     const int64_t size = part_floats<D, NT>();
     const float* base = a.part + int64_t(ds.cta) * 2 * size + r * stride;
-    auto piece = [&](int p) { return base + (p == 0 ? size : 2 * size * p); };
-    float m = -INFINITY, l = 0.f;
-    for (int p = threadIdx.x; p < ds.pieces; p += kJoin) m = fmaxf(m, piece(p)[D]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) red[0][warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoin / 32; ++w) m = fmaxf(m, red[0][w]);
-    const float top = m == -INFINITY ? 0.f : m;
-    for (int p = threadIdx.x; p < ds.pieces; p += kJoin) l += exp2f(piece(p)[D] - top) * piece(p)[D + 1];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) red[1][warp] = l;
     const int d = threadIdx.x % D, part = threadIdx.x / D;
-    float o = 0.f;
-#pragma unroll 8
-    for (int p = part; p < ds.pieces; p += kPar) o += exp2f(piece(p)[D] - top) * piece(p)[d];
-    sum[part][d] = o;
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    for (int p0 = part; p0 < ds.pieces; p0 += kBatch * kPar) {
+        float pm[kBatch], pl[kBatch], po[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int p = p0 + i * kPar;
+            const float* from = base + (p == 0 ? size : 2 * size * p);
+            const bool there = p < ds.pieces;
+            pm[i] = there ? from[D] : -INFINITY;
+            pl[i] = there ? from[D + 1] : 0.f;
+            po[i] = there ? from[d] : 0.f;
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, pm[i]);
+        const float base2 = top == -INFINITY ? 0.f : top, f = ex2(m - base2);
+        l *= f;
+        o *= f;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float e = ex2(pm[i] - base2);
+            l += e * pl[i];
+            o += e * po[i];
+        }
+        m = top;
+    }
+    sm_o[part][d] = o;
+    if (d == 0) {
+        sm_m[part] = m;
+        sm_l[part] = l;
+    }
     __syncthreads();
     if (part) return;
-    l = 0.f;
+    float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kJoin / 32; ++w) l += red[1][w];
+    for (int i = 0; i < kPar; ++i) top = fmaxf(top, sm_m[i]);
+    const float base2 = top == -INFINITY ? 0.f : top;
+    l = o = 0.f;
 #pragma unroll
-    for (int i = 1; i < kPar; ++i) o += sum[i][d];
+    for (int i = 0; i < kPar; ++i) {
+        const float e = ex2(sm_m[i] - base2);
+        l += e * sm_l[i];
+        o += e * sm_o[i][d];
+    }
     a.o[((int64_t(ds.b) * a.T + R / a.G) * a.heads + ds.h * a.G + R % a.G) * D + d] = __float2half_rn(l == 0.f ? 0.f : o / l);
 }
 

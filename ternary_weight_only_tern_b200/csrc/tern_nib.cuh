@@ -28,6 +28,57 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8) {
     return as_u32(__hfma2(h, as_h2(0x2C002C00u), as_h2(kBias ? 0xD480D480u : 0xD400D400u)));       // / 16 - 72 or - 64
 }
 
+// Pair P of a word's codes plus 64, exactly: codes in bits 4-7 under the exponent of 64 count 1 each; those in bits
+// 0-3 come under that of 1024 and lose 960. Two operations fewer a word than code_pair; what the 64 add to a product,
+// 64 times the other factor's sum, is taken off in fp32 behind the sum.
+template <int P>
+__device__ __forceinline__ uint32_t code_pair_64(uint32_t w, uint32_t w8) {
+    const uint32_t v = P < 2 ? w : w8;
+    if (P & 1) return lop3_and_or(v, 0x00F000F0u, 0x54005400u);
+    return as_u32(__hsub2(as_h2(lop3_and_or(v, 0x000F000Fu, 0x64006400u)), as_h2(0x63806380u)));
+}
+
+// D += A . B for one m16n8k16 tile, fp16 inputs, fp32 accumulators. Not volatile: the compiler may move it among the
+// loads and decodes of other steps.
+__device__ __forceinline__ void mma_next(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// D = A . B: the first step of a sum, with nothing to clear.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// D += A . B for one m16n8k8 tile of tf32 values held in fp32: fp16 numbers are exact in it. Lane 4 g + q holds
+// A (rows g and g + 8, column q), (.., column q + 4) and B (row q, column g), (row q + 4, column g).
+__device__ __forceinline__ void mma_1688(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+    asm(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+__device__ __forceinline__ void mma_1688_first(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+    asm(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)), "f"(0.f));
+}
+
+// v = hi + lo, each a tf32 number, but for 2^-22 v.
+__device__ __forceinline__ float tf32_part(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFFE000u); }
+
 // Code of x for step s and zero z: rint((x - z) / s) + bias in 0 .. 15, the quotient rounded to fp32 first;
 // inv = 1 / s to fp32. t is within 1e-5 of that quotient for every |t| < 32, so unless it lies next to a
 // tie both round to the same integer; the division is done only there.
