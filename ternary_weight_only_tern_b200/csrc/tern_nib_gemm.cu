@@ -1,92 +1,389 @@
-// y [M, N] = x [M, K] . W^T for a 4-bit W = mu + s (c - 8) (tern.h has the layout).
+// y [M, N] = x [M, K] . W^T for a 4-bit W = mu + s (c - 8) and more than 16 tokens, on tcgen05 tensor cores, W
+// dequantised from its codes straight into shared memory (tern.h has the layout).
 //
-// One warp takes a strip of 16 rows and 8 tokens: mma.sync m16n8k16 with the strip's codes as A (exact in fp16)
-// and the tokens as B's columns, fp32 accumulators per group, then
-//   y[m, n] = sum_g s[n, g] sum_k (c - 8) x + mu[n, g] sum_k x,
-// the second sum from the same instruction with A = 1.
+// A CTA computes 128 H weight rows x BT tokens: H tcgen05.mma (kind::f16, M = 128, N = BT, K = 16) per 16 columns of K
+// with the weights as A and the tokens as B, fp32 accumulators in H 256 columns of TMEM. Weights as rows: the few
+// tokens of a small batch cost few columns, and the layout's 16-byte vectors (32 codes of a row) fit the rows.
+//  * warp 0, one thread: TMA loads of the x tile (BT x 64 fp16, 128-byte swizzle) into the stages;
+//  * warp 1, one thread: issues the MMAs and commits each stage back;
+//  * warps 2-9: decode. A lane loads its vectors and scales of the next 128 columns while it works on these, two stages of 64:
+//    eight codes are five integer and four fp16 operations, w = rn16(mu + s (c - 8)) four more, and leave as one 16-byte
+//    store. Rows of odd index store the other half's word first, so that a quarter warp's stores hit all banks
+//    once. The same warps bring the accumulators out of TMEM.
+// Tile and slices of K are chosen per call by a cost of both sides (plan_of): waves of CTAs times the slower of the MMAs and the
+// decoding. The slices' sums go to the workspace in fp32 and are added in order by a second kernel.
+#include <algorithm>
+#include <mutex>
+
 #include "tern_nib.cuh"
 
 namespace tern {
+namespace nib {
+
+void add_slices(const float* part, int slices, int64_t n, __half* y, cudaStream_t stream, cudaError_t& err);   // tern_nib_linear.cu
+
+}  // namespace nib
+
 namespace {
 
 using namespace nib;
 
-constexpr int kWarps = 4;
+constexpr int kDecodeWarps = 8;
+constexpr int kThreads = (2 + kDecodeWarps) * 32;
+constexpr int kMaxStages = 6;
+constexpr int kRowsM = 128;                // rows of an MMA
+constexpr int kBK = 64;
+constexpr int kABytes = kRowsM * kBK * 2;
+constexpr int kSmemMax = 227 * 1024;
 
-template <int kGrp>
-__global__ void __launch_bounds__(kWarps * 32) linear_kernel(const uint32_t* __restrict__ codes,
-                                                             const __half* __restrict__ scale,
-                                                             const __half* __restrict__ mu, int64_t N, int64_t K,
-                                                             const __half* __restrict__ x, int64_t M,
-                                                             __half* __restrict__ y) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int64_t strip = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5), KB = K / kGroup;
-    const int64_t m0 = int64_t(blockIdx.y) * 8;
-    if (strip * 16 >= N) return;
-    const bool token = m0 + g < M;
-    const __half* xr = x + (token ? m0 + g : 0) * K + 8 * q;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int span = kGrp / 32;
-    for (int64_t kb = 0; kb < KB; ++kb) {
-        const uint32_t* block = codes + (strip * KB + kb) * kBlockWords + lane * 4;
-        const uint4 va = __ldg(reinterpret_cast<const uint4*>(block));
-        const uint4 vb = __ldg(reinterpret_cast<const uint4*>(block + 128));
-        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+struct Args {
+    const uint32_t* codes;
+    const __half* scale;
+    const __half* mu;
+    __half* y;
+    float* part;               // [gridDim.z][M][N], or nullptr
+    int64_t N, M;
+    int KB, strips, slice;     // blocks of 128 columns; of a slice
+    int bt, stages, stage_bytes;
+    int early;
+    unsigned int* status;
+};
+
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr) {
+    return ((uint64_t(addr) & 0x3FFFFull) >> 4) | (1ull << 16) | (uint64_t(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void load_tmem32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+        "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+template <int kGrp, int H>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const Args a) {
+    constexpr int per = kGroup / kGrp, V = 2 * H;        // groups of a block; a lane's vectors of a block
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full_x[kMaxStages], full_w[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint32_t tmem_slot;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t n0 = int64_t(blockIdx.x) * kRowsM * H, m0 = int64_t(blockIdx.y) * a.bt;
+    const int kb0 = int(blockIdx.z) * a.slice, nb = min(a.slice, a.KB - kb0), steps = 2 * nb;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(&full_x[s], 1);
+            mbar_init(&full_w[s], kDecodeWarps);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(256 * H) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot, base = smem_u32(smem);
+    grid_launch_dependents();
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            grid_dependency_wait();
+            int issued = 0;
+            for (int i = 0, s = 0, ph = 1; i < steps; ++i) {
+                if (i >= a.stages) ok = mbar_wait(&empty[s], ph);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&full_x[s], uint32_t(a.bt * kBK * 2));
+                tma_load_2d(smem + s * a.stage_bytes + H * kABytes, &tmap_x, (kb0 * 2 + i) * kBK, int(m0), &full_x[s]);
+                issued = i + 1;
+                if (++s == a.stages) s = 0, ph ^= 1;
+            }
+            // every copy lands before the CTA may end
+            for (int i = max(0, issued - a.stages); i < issued; ++i)
+                if (!mbar_wait(&full_x[i % a.stages], (i / a.stages) & 1)) ok = false;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = (1u << 4) | (uint32_t(a.bt >> 3) << 17) | (uint32_t(kRowsM >> 4) << 24);
+            for (int i = 0, s = 0, ph = 0; i < steps; ++i) {
+                ok = mbar_wait(&full_x[s], ph) && mbar_wait(&full_w[s], ph);
+                if (!ok) break;
+                fence_after();
+                const uint32_t at = base + s * a.stage_bytes;
 #pragma unroll
-        for (int j0 = 0; j0 < 4; j0 += span) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f}, ones[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < kBK / 16; ++k) {
+                    const uint64_t b = matrix_desc(at + H * kABytes + 32 * k);
 #pragma unroll
-            for (int j = j0; j < j0 + span; ++j) {
-                const uint4 b = token ? __ldg(reinterpret_cast<const uint4*>(xr + kb * kGroup + 32 * j))
-                                      : make_uint4(0, 0, 0, 0);
-                const uint32_t a8 = wa[j] >> 8, b8 = wb[j] >> 8;
-                const uint32_t A0[4] = {code_pair<0, 8>(wa[j], a8), code_pair<0, 8>(wb[j], b8),
-                                        code_pair<1, 8>(wa[j], a8), code_pair<1, 8>(wb[j], b8)};
-                const uint32_t A1[4] = {code_pair<2, 8>(wa[j], a8), code_pair<2, 8>(wb[j], b8),
-                                        code_pair<3, 8>(wa[j], a8), code_pair<3, 8>(wb[j], b8)};
-                const uint32_t one[4] = {kHalf2One, kHalf2One, kHalf2One, kHalf2One};
-                mma_16816(acc, A0, b.x, b.y);
-                mma_16816(acc, A1, b.z, b.w);
-                if (mu) {
-                    mma_16816(ones, one, b.x, b.y);
-                    mma_16816(ones, one, b.z, b.w);
+                    for (int h = 0; h < H; ++h) mma_f16(tmem + 256 * h, matrix_desc(at + h * kABytes + 32 * k), b, idesc, i > 0 || k > 0);
+                }
+                commit(&empty[s]);
+                if (++s == a.stages) s = 0, ph ^= 1;
+            }
+            commit(&done);          // also after a timeout: every issued MMA retires first
+            if (!mbar_wait(&done, 0)) ok = false;
+        }
+    } else {
+        // ---- decode: the warp's H strips of the tile, both halves of each; vector v: strip v / 2, rows 8 (v % 2) + g
+        const int dw = warp - 2, g = lane >> 2, q = lane & 3;
+        const uint4* from[H];
+        const __half2* sc[H];
+        const __half2* mu[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int64_t strip = min(n0 / 16 + dw * H + h, int64_t(a.strips) - 1), blk = strip * a.KB + kb0;
+            from[h] = reinterpret_cast<const uint4*>(a.codes + blk * kBlockWords) + lane;
+            sc[h] = reinterpret_cast<const __half2*>(a.scale + blk * per * 16) + g;
+            mu[h] = a.mu ? reinterpret_cast<const __half2*>(a.mu + blk * per * 16) + g : nullptr;
+        }
+        if (!a.early) grid_dependency_wait();
+        uint4 next[V];
+        __half2 sn[H][per], mn[H][per];
+        auto load = [&](int kb) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                next[2 * h] = __ldg(from[h] + kb * (kBlockWords / 4));
+                next[2 * h + 1] = __ldg(from[h] + kb * (kBlockWords / 4) + 32);
+#pragma unroll
+                for (int p = 0; p < per; ++p) {
+                    sn[h][p] = __ldg(sc[h] + (kb * per + p) * 8);
+                    if (a.mu) mn[h][p] = __ldg(mu[h] + (kb * per + p) * 8);
                 }
             }
-            const int64_t at = ((strip * KB + kb) * (kGroup / kGrp) + j0 / span) * 16 + 2 * g;
-            const float2 s = __half22float2(__ldg(reinterpret_cast<const __half2*>(scale + at)));
-            sum[0] += s.x * acc[0];
-            sum[1] += s.x * acc[1];
-            sum[2] += s.y * acc[2];
-            sum[3] += s.y * acc[3];
-            if (mu) {
-                const float2 m = __half22float2(__ldg(reinterpret_cast<const __half2*>(mu + at)));
-                sum[0] += m.x * ones[0];
-                sum[1] += m.x * ones[1];
-                sum[2] += m.y * ones[2];
-                sum[3] += m.y * ones[3];
+        };
+        const bool swap = g & 1;
+        // row r of the warp's strips within the tile: 16 (dw H + h) + 8 (v % 2) + g
+        uint32_t to[2];             // of the lane's two chunks (words 0 and 1 of a stage), row 16 dw H + g
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int chunk = 4 * (swap ? 1 - e : e) + q;
+            to[e] = uint32_t(16 * dw * H + g) * 128 + uint32_t((chunk ^ g) << 4);
+        }
+        load(0);
+        int s = 0, ph = 1;
+        for (int kb = 0; kb < nb && ok; ++kb) {
+            uint4 cur[V];
+            __half2 sv[H][per], mv[H][per];
+#pragma unroll
+            for (int v = 0; v < V; ++v) cur[v] = next[v];
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int p = 0; p < per; ++p) {
+                    sv[h][p] = sn[h][p];
+                    mv[h][p] = a.mu ? mn[h][p] : __half2half2(__float2half_rn(0.f));
+                }
+            if (kb + 1 < nb) load(kb + 1);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (2 * kb + half >= a.stages) ok = ok && mbar_wait(&empty[s], ph);
+                const uint32_t at = base + s * a.stage_bytes;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const uint32_t w0 = half ? cur[v].z : cur[v].x, w1 = half ? cur[v].w : cur[v].y;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w = (e == 0) == !swap ? w0 : w1, w8 = w >> 8;
+                        // its group of the block: column 64 half + 32 (word)
+                        const int p0 = (64 * half) / kGrp, p1 = (64 * half + 32) / kGrp;
+                        const bool second = (e == 1) != swap;
+                        const __half2 sr = p0 == p1 ? sv[v >> 1][p0] : second ? sv[v >> 1][p1] : sv[v >> 1][p0];
+                        const __half2 mr = p0 == p1 ? mv[v >> 1][p0] : second ? mv[v >> 1][p1] : mv[v >> 1][p0];
+                        const __half2 s2 = (v & 1) ? __high2half2(sr) : __low2half2(sr), m2 = (v & 1) ? __high2half2(mr) : __low2half2(mr);
+                        const uint4 o = make_uint4(as_u32(__hfma2(as_h2(code_pair<0, 8>(w, w8)), s2, m2)),
+                                                   as_u32(__hfma2(as_h2(code_pair<1, 8>(w, w8)), s2, m2)),
+                                                   as_u32(__hfma2(as_h2(code_pair<2, 8>(w, w8)), s2, m2)),
+                                                   as_u32(__hfma2(as_h2(code_pair<3, 8>(w, w8)), s2, m2)));
+                        sts_u4(at + to[e] + uint32_t((v >> 1) * 16 + (v & 1) * 8) * 128, o);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full_w[s]);
+                if (++s == a.stages) s = 0, ph ^= 1;
+            }
+        }
+        if (a.early) grid_dependency_wait();       // y may still be in use by the previous kernel
+        // ---- epilogue
+        ok = ok && mbar_wait(&done, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        fence_after();
+        if (ok) {
+            const int lq = warp & 3, hi = dw >> 2, half = H == 2 ? hi : 0;
+            const int c0 = H == 2 ? 0 : hi * ((a.bt / 2 + 31) / 32 * 32), c1 = H == 2 || hi ? a.bt : min(a.bt, (a.bt / 2 + 31) / 32 * 32);
+            const int64_t n = n0 + half * kRowsM + lq * 32 + lane;
+            const bool pairs = (a.N & 1) == 0 && !a.part;
+            for (int c = c0; c < c1; c += 32) {
+                uint32_t r[32];
+                load_tmem32(tmem + (uint32_t(lq * 32) << 16) + uint32_t(half * 256 + c), r);
+                const int64_t m = m0 + c;
+                const int cnt = int(min(int64_t(min(32, c1 - c)), a.M - m));
+                if (pairs) {
+                    // even lanes take the even token of a pair for rows n and n + 1, odd lanes the odd one
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? r[j] : r[j + 1], 1);
+                        const int mine = j + (lane & 1);
+                        const __half2 v = lane & 1 ? __floats2half2_rn(__uint_as_float(got), __uint_as_float(r[j + 1]))
+                                                   : __floats2half2_rn(__uint_as_float(r[j]), __uint_as_float(got));
+                        if (mine < cnt && n < a.N) *reinterpret_cast<__half2*>(a.y + (m + mine) * a.N + (n & ~int64_t(1))) = v;
+                    }
+                } else if (n < a.N) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (j < cnt) {
+                            if (a.part) a.part[(int64_t(blockIdx.z) * a.M + m + j) * a.N + n] = __uint_as_float(r[j]);
+                            else a.y[(m + j) * a.N + n] = __float2half_rn(__uint_as_float(r[j]));
+                        }
+                    }
+                }
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t n = strip * 16 + g + 8 * (i >> 1), m = m0 + 2 * q + (i & 1);
-        if (n < N && m < M) y[m * N + n] = __float2half_rn(sum[i]);
+    __syncwarp();
+    if (!ok && a.status) atomicOr(a.status, kStatusTimeout);
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256 * H) : "memory");
     }
+}
+
+// ---------------------------------------------------------------- the plan of a call
+struct Plan {
+    int h, bt, slices, slice, stages, stage_bytes;
+};
+
+// Cycles of a call on the SMs: waves of CTAs, each 64 columns of K as long as the slower of its MMAs (2 bt per 128 rows) and
+// its decoding (about 260 per 128 rows), about 3000 for a CTA's start and end; slices of K add a kernel and their sums' way
+// through memory.
+Plan plan_of(const tern_nib_weight& w, int64_t M) {
+    const int KB = int(w.K / kGroup);
+    const int64_t sms = sm_count();
+    Plan best{};
+    double least = 1e30;
+    for (int h = 1; h <= 2; ++h)
+        for (int bt = 16; bt <= 256; bt += 16) {
+            if (bt < 256 && bt < 128 && bt < M) continue;                // few tokens: all in one tile
+            if (bt >= 32 && int64_t(bt - 16) >= M) break;
+            for (int slices = 1; slices <= 8 && slices <= KB; slices *= 2) {
+                const int slice = (KB + slices - 1) / slices, real = (KB + slice - 1) / slice;
+                const int64_t rows = (w.N + kRowsM * h - 1) / (kRowsM * h), toks = (M + bt - 1) / bt;
+                const int64_t waves = (rows * toks * real + sms - 1) / sms;
+                double c = double(waves) * (2.0 * slice * h * std::max(2.0 * bt, 260.0) + 3000.0);
+                if (real > 1) c += 4000.0 + 8.0 * double(real) * double(M) * double(w.N) / (30.0 * double(sms));
+                if (c < least) {
+                    least = c;
+                    best = Plan{h, bt, real, slice, 0, 0};
+                }
+            }
+        }
+    best.stage_bytes = best.h * kABytes + best.bt * kBK * 2;
+    best.stages = std::min(kMaxStages, (kSmemMax - 2048) / best.stage_bytes);
+    return best;
+}
+
+template <int kGrp, int H>
+tern_status launch(const Plan& p, const tern_nib_weight& w, const CUtensorMap& map, Args& a, cudaStream_t stream) {
+    static std::mutex mu;
+    static bool configured[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TERN_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!configured[dev]) {
+            if (cudaFuncSetAttribute(gemm_kernel<kGrp, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 1024) != cudaSuccess)
+                return TERN_ERR_CUDA;
+            configured[dev] = true;
+        }
+    }
+    const int64_t rows = (w.N + kRowsM * H - 1) / (kRowsM * H), toks = (a.M + p.bt - 1) / p.bt;
+    if (toks > 65535) return TERN_ERR_SHAPE;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(rows), unsigned(toks), unsigned(p.slices));
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = size_t(p.stages) * p.stage_bytes + 1024;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<kGrp, H>, map, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
 }  // namespace
 
 namespace nib {
 
-tern_status gemm_launch(const tern_nib_weight& w, const __half* x, int64_t M, __half* y, cudaStream_t stream) {
-    if ((M + 7) / 8 > 65535) return TERN_ERR_SHAPE;
-    const dim3 grid(unsigned(((w.N + 15) / 16 + kWarps - 1) / kWarps), unsigned((M + 7) / 8), 1);
-    auto kernel = w.group == 32 ? linear_kernel<32> : w.group == 64 ? linear_kernel<64> : linear_kernel<128>;
-    kernel<<<grid, kWarps * 32, 0, stream>>>(w.codes, reinterpret_cast<const __half*>(w.scale),
-                                             reinterpret_cast<const __half*>(w.mu), w.N, w.K, x, M, y);
-    return launched();
+size_t gemm_workspace_bytes(const tern_nib_weight& w, int64_t M) {
+    const Plan p = plan_of(w, M);
+    return p.slices == 1 ? 0 : (size_t(p.slices) * size_t(M) * size_t(w.N) * 4 + 255) & ~size_t(255);
+}
+
+tern_status gemm_launch(const tern_nib_weight& w, const __half* x, int64_t M, __half* y, void* workspace, cudaStream_t stream) {
+    const Plan p = plan_of(w, M);
+    auto enc = encode_fn();
+    if (!enc) return TERN_ERR_CUDA;
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {cuuint64_t(w.K), cuuint64_t(M)};
+    const cuuint64_t strides[1] = {cuuint64_t(w.K) * sizeof(__half)};
+    const cuuint32_t box[2] = {kBK, cuuint32_t(p.bt)}, estr[2] = {1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(x), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return TERN_ERR_CUDA;
+    Args a{};
+    a.codes = w.codes;
+    a.scale = reinterpret_cast<const __half*>(w.scale);
+    a.mu = reinterpret_cast<const __half*>(w.mu);
+    a.y = y;
+    a.part = p.slices > 1 ? static_cast<float*>(workspace) : nullptr;
+    a.N = w.N;
+    a.M = M;
+    a.KB = int(w.K / kGroup);
+    a.strips = int((w.N + 15) / 16);
+    a.slice = p.slice;
+    a.bt = p.bt;
+    a.stages = p.stages;
+    a.stage_bytes = p.stage_bytes;
+    a.early = (w.flags & TERN_WEIGHT_STATIC) != 0;
+    a.status = async_status_word();
+    tern_status st;
+    if (p.h == 1) st = w.group == 32 ? launch<32, 1>(p, w, map, a, stream) : w.group == 64 ? launch<64, 1>(p, w, map, a, stream) : launch<128, 1>(p, w, map, a, stream);
+    else st = w.group == 32 ? launch<32, 2>(p, w, map, a, stream) : w.group == 64 ? launch<64, 2>(p, w, map, a, stream) : launch<128, 2>(p, w, map, a, stream);
+    if (st != TERN_OK || p.slices == 1) return st;
+    cudaError_t err;
+    add_slices(a.part, p.slices, M * w.N, y, stream, err);
+    return err == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
 }  // namespace nib
 }  // namespace tern
-

@@ -28,7 +28,10 @@
 namespace tern {
 namespace nib {
 
-tern_status gemm_launch(const tern_nib_weight& w, const __half* x, int64_t M, __half* y, cudaStream_t stream);   // tern_nib_gemm.cu
+// tern_nib_gemm.cu
+tern_status gemm_launch(const tern_nib_weight& w, const __half* x, int64_t M, __half* y, void* workspace, cudaStream_t stream);
+void add_slices(const float* part, int slices, int64_t n, __half* y, cudaStream_t stream, cudaError_t& err);
+size_t gemm_workspace_bytes(const tern_nib_weight& w, int64_t M);
 
 }  // namespace nib
 
@@ -295,6 +298,27 @@ __global__ void __launch_bounds__(256) add_kernel(const float* __restrict__ part
     y[i] = __float2half_rn(f);
 }
 
+}  // namespace
+
+namespace nib {
+
+void add_slices(const float* part, int slices, int64_t n, __half* y, cudaStream_t stream, cudaError_t& err) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((n + 255) / 256), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, add_kernel, part, slices, n, y);
+}
+
+}  // namespace nib
+
+namespace {
+
 // ---------------------------------------------------------------- the plan of a call
 constexpr int kSmemMax = 227 * 1024;
 
@@ -366,11 +390,9 @@ tern_status launch(const Plan& p, Args& a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, linear_kernel<kGrp, NT>, a) != cudaSuccess) return TERN_ERR_CUDA;
     if (p.slices == 1) return TERN_OK;
-    const int64_t n = int64_t(a.M) * a.N;
-    cfg.gridDim = dim3(unsigned((n + 255) / 256), 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, add_kernel, static_cast<const float*>(a.part), p.slices, n, a.y) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
+    cudaError_t err;
+    add_slices(a.part, p.slices, int64_t(a.M) * a.N, a.y, stream, err);
+    return err == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
 }  // namespace
@@ -380,8 +402,10 @@ using namespace tern;
 using namespace tern::nib;
 
 extern "C" size_t tern_nib_linear_workspace_bytes(const tern_nib_weight* w, int64_t M) {
+    if (check_nib(w) != TERN_OK || M <= 0) return 0;
+    if (M > kMaxM) return gemm_workspace_bytes(*w, M);
     Plan p;
-    if (check_nib(w) != TERN_OK || M <= 0 || M > kMaxM || !plan_of(*w, int(M), p) || p.slices == 1) return 0;
+    if (!plan_of(*w, int(M), p) || p.slices == 1) return 0;
     return (size_t(p.slices) * size_t(M) * size_t(w->N) * 4 + 255) & ~size_t(255);
 }
 
@@ -400,7 +424,7 @@ extern "C" tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half
     const __half* xh = reinterpret_cast<const __half*>(x);
     __half* yh = reinterpret_cast<__half*>(y);
     cudaStream_t cs = as_cuda(stream);
-    if (M > kMaxM) return gemm_launch(*w, xh, M, yh, cs);
+    if (M > kMaxM) return gemm_launch(*w, xh, M, yh, workspace, cs);
     Plan p;
     if (!plan_of(*w, int(M), p)) return TERN_ERR_SHAPE;
     Args a{};
