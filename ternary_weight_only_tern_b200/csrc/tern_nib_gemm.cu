@@ -28,8 +28,9 @@ namespace {
 
 using namespace nib;
 
-constexpr int kDecodeWarps = 8;
+constexpr int kDecodeWarps = 16;
 constexpr int kThreads = (2 + kDecodeWarps) * 32;
+constexpr int kAhead = 2;                  // blocks of 128 columns that a decoding lane loads ahead of its own
 constexpr int kMaxStages = 6;
 constexpr int kRowsM = 128;                // rows of an MMA
 constexpr int kBK = 64;
@@ -54,17 +55,24 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr) {
     return ((uint64_t(addr) & 0x3FFFFull) >> 4) | (1ull << 16) | (uint64_t(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// One MMA, issued by one lane of a converged warp: the operands are then uniform registers as they stand (issued from a
+// single-lane branch each took about 90 cycles to gather them).
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -84,9 +92,9 @@ __device__ __forceinline__ void load_tmem32(uint32_t addr, uint32_t (&r)[32]) {
 
 template <int kGrp, int H>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const Args a) {
-    constexpr int per = kGroup / kGrp, V = 2 * H;        // groups of a block; a lane's vectors of a block
+    constexpr int per = kGroup / kGrp;                   // groups of a block
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full_x[kMaxStages], full_w[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t tmem_slot;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -95,8 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(&full_x[s], 1);
-            mbar_init(&full_w[s], kDecodeWarps);
+            mbar_init(&full[s], 8 * H + 1);     // the decoding warps and x's loader
             mbar_init(&empty[s], 1);
         }
         mbar_init(&done, 1);
@@ -120,113 +127,116 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int i = 0, s = 0, ph = 1; i < steps; ++i) {
                 if (i >= a.stages) ok = mbar_wait(&empty[s], ph);
                 if (!ok) break;
-                mbar_arrive_expect_tx(&full_x[s], uint32_t(a.bt * kBK * 2));
-                tma_load_2d(smem + s * a.stage_bytes + H * kABytes, &tmap_x, (kb0 * 2 + i) * kBK, int(m0), &full_x[s]);
+                mbar_arrive_expect_tx(&full[s], uint32_t(a.bt * kBK * 2));
+                tma_load_2d(smem + s * a.stage_bytes + H * kABytes, &tmap_x, (kb0 * 2 + i) * kBK, int(m0), &full[s]);
                 issued = i + 1;
                 if (++s == a.stages) s = 0, ph ^= 1;
             }
             // every copy lands before the CTA may end
-            for (int i = max(0, issued - a.stages); i < issued; ++i)
-                if (!mbar_wait(&full_x[i % a.stages], (i / a.stages) & 1)) ok = false;
+            for (int i = max(0, issued - a.stages); i < issued; ++i) ok = mbar_wait_for(&full[i % a.stages], (i / a.stages) & 1, ok ? kWaitLimitCycles : kWaitLimitCycles / 64) && ok;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = (1u << 4) | (uint32_t(a.bt >> 3) << 17) | (uint32_t(kRowsM >> 4) << 24);
-            for (int i = 0, s = 0, ph = 0; i < steps; ++i) {
-                ok = mbar_wait(&full_x[s], ph) && mbar_wait(&full_w[s], ph);
-                if (!ok) break;
-                fence_after();
-                const uint32_t at = base + s * a.stage_bytes;
+        const uint32_t idesc = (1u << 4) | (uint32_t(a.bt >> 3) << 17) | (uint32_t(kRowsM >> 4) << 24);
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0), at0 = __shfl_sync(0xffffffffu, base, 0);
+        const uint32_t empty_at = __shfl_sync(0xffffffffu, smem_u32(empty), 0);
+        for (int i = 0, s = 0, ph = 0; i < steps; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph));
+            if (!ok) break;
+            fence_after();
+            const uint32_t at = at0 + s * a.stage_bytes;
+            const uint64_t wd = matrix_desc(at), xd = matrix_desc(at + H * kABytes);      // + 2: 32 bytes on
 #pragma unroll
-                for (int k = 0; k < kBK / 16; ++k) {
-                    const uint64_t b = matrix_desc(at + H * kABytes + 32 * k);
+            for (int k = 0; k < kBK / 16; ++k)
 #pragma unroll
-                    for (int h = 0; h < H; ++h) mma_f16(tmem + 256 * h, matrix_desc(at + h * kABytes + 32 * k), b, idesc, i > 0 || k > 0);
-                }
-                commit(&empty[s]);
-                if (++s == a.stages) s = 0, ph ^= 1;
-            }
-            commit(&done);          // also after a timeout: every issued MMA retires first
-            if (!mbar_wait(&done, 0)) ok = false;
+                for (int h = 0; h < H; ++h) mma_f16(d + 256 * h, wd + (h * kABytes >> 4) + 2 * k, xd + 2 * k, idesc, i > 0 || k > 0);
+            commit(empty_at + s * 8);
+            if (++s == a.stages) s = 0, ph ^= 1;
         }
+        commit(smem_u32(&done));          // also after a timeout: every issued MMA retires first
+        if (!mbar_wait(&done, 0)) ok = false;
     } else {
-        // ---- decode: the warp's H strips of the tile, both halves of each; vector v: strip v / 2, rows 8 (v % 2) + g
-        const int dw = warp - 2, g = lane >> 2, q = lane & 3;
-        const uint4* from[H];
-        const __half2* sc[H];
-        const __half2* mu[H];
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const int64_t strip = min(n0 / 16 + dw * H + h, int64_t(a.strips) - 1), blk = strip * a.KB + kb0;
-            from[h] = reinterpret_cast<const uint4*>(a.codes + blk * kBlockWords) + lane;
-            sc[h] = reinterpret_cast<const __half2*>(a.scale + blk * per * 16) + g;
-            mu[h] = a.mu ? reinterpret_cast<const __half2*>(a.mu + blk * per * 16) + g : nullptr;
-        }
+        // ---- decode: a strip of the tile per warp, every block of 128 columns or (H = 1) every other; vector v: rows
+        // 8 v + g. With one MMA per step two stages are filled at a time, so that the proxy fence and the hand-over, which take
+        // longer than the decoding, are paid once for both.
+        constexpr int kStep = 2 / H, kAtOnce = H == 1 ? 2 : 1;
+        const int dw = (warp - 2) % (8 * H), first = (warp - 2) / (8 * H), g = lane >> 2, q = lane & 3;
+        const int64_t strip = min(n0 / 16 + dw, int64_t(a.strips) - 1), blk = strip * a.KB + kb0;
+        const uint4* from = reinterpret_cast<const uint4*>(a.codes + blk * kBlockWords) + lane;
+        const __half2* sc = reinterpret_cast<const __half2*>(a.scale + blk * per * 16) + g;
+        const __half2* mu = a.mu ? reinterpret_cast<const __half2*>(a.mu + blk * per * 16) + g : nullptr;
         if (!a.early) grid_dependency_wait();
-        uint4 next[V];
-        __half2 sn[H][per], mn[H][per];
-        auto load = [&](int kb) {
+        uint4 next[kAhead][2];
+        __half2 sn[kAhead][per], mn[kAhead][per];
+        auto load = [&](int at, int kb) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                next[2 * h] = __ldg(from[h] + kb * (kBlockWords / 4));
-                next[2 * h + 1] = __ldg(from[h] + kb * (kBlockWords / 4) + 32);
+            for (int v = 0; v < 2; ++v) next[at][v] = __ldg(from + kb * (kBlockWords / 4) + 32 * v);
 #pragma unroll
-                for (int p = 0; p < per; ++p) {
-                    sn[h][p] = __ldg(sc[h] + (kb * per + p) * 8);
-                    if (a.mu) mn[h][p] = __ldg(mu[h] + (kb * per + p) * 8);
-                }
+            for (int p = 0; p < per; ++p) {
+                sn[at][p] = __ldg(sc + (kb * per + p) * 8);
+                if (a.mu) mn[at][p] = __ldg(mu + (kb * per + p) * 8);
             }
         };
         const bool swap = g & 1;
-        // row r of the warp's strips within the tile: 16 (dw H + h) + 8 (v % 2) + g
-        uint32_t to[2];             // of the lane's two chunks (words 0 and 1 of a stage), row 16 dw H + g
+        uint32_t to[2];             // of the lane's two chunks (words 0 and 1 of a stage), row 16 dw + g of the tile
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int chunk = 4 * (swap ? 1 - e : e) + q;
-            to[e] = uint32_t(16 * dw * H + g) * 128 + uint32_t((chunk ^ g) << 4);
+            to[e] = uint32_t(16 * dw + g) * 128 + uint32_t((chunk ^ g) << 4);
         }
-        load(0);
-        int s = 0, ph = 1;
-        for (int kb = 0; kb < nb && ok; ++kb) {
-            uint4 cur[V];
-            __half2 sv[H][per], mv[H][per];
 #pragma unroll
-            for (int v = 0; v < V; ++v) cur[v] = next[v];
+        for (int i = 0; i < kAhead; ++i)
+            if (first + i * kStep < nb) load(i, first + i * kStep);
+        int s = 2 * first % a.stages, ph = 1 ^ (2 * first / a.stages & 1);
+        for (int kbase = first; kbase < nb && ok; kbase += kAhead * kStep) {
 #pragma unroll
-            for (int h = 0; h < H; ++h)
+            for (int i = 0; i < kAhead; ++i) {
+                const int kb = kbase + i * kStep;
+                if (kb >= nb || !ok) break;
+                uint4 cur[2] = {next[i][0], next[i][1]};
+                __half2 sv[per], mv[per];
 #pragma unroll
                 for (int p = 0; p < per; ++p) {
-                    sv[h][p] = sn[h][p];
-                    mv[h][p] = a.mu ? mn[h][p] : __half2half2(__float2half_rn(0.f));
+                    sv[p] = sn[i][p];
+                    mv[p] = a.mu ? mn[i][p] : __half2half2(__float2half_rn(0.f));
                 }
-            if (kb + 1 < nb) load(kb + 1);
+                if (kb + kAhead * kStep < nb) load(i, kb + kAhead * kStep);
+                int held = s;       // the first stage not yet handed over
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (2 * kb + half >= a.stages) ok = ok && mbar_wait(&empty[s], ph);
-                const uint32_t at = base + s * a.stage_bytes;
+                for (int half = 0; half < 2; ++half) {
+                    if (2 * kb + half >= a.stages) ok = ok && mbar_wait(&empty[s], ph);
+                    const uint32_t at = base + s * a.stage_bytes;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const uint32_t w0 = half ? cur[v].z : cur[v].x, w1 = half ? cur[v].w : cur[v].y;
+                    for (int v = 0; v < 2; ++v) {
+                        const uint32_t w0 = half ? cur[v].z : cur[v].x, w1 = half ? cur[v].w : cur[v].y;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t w = (e == 0) == !swap ? w0 : w1, w8 = w >> 8;
-                        // its group of the block: column 64 half + 32 (word)
-                        const int p0 = (64 * half) / kGrp, p1 = (64 * half + 32) / kGrp;
-                        const bool second = (e == 1) != swap;
-                        const __half2 sr = p0 == p1 ? sv[v >> 1][p0] : second ? sv[v >> 1][p1] : sv[v >> 1][p0];
-                        const __half2 mr = p0 == p1 ? mv[v >> 1][p0] : second ? mv[v >> 1][p1] : mv[v >> 1][p0];
-                        const __half2 s2 = (v & 1) ? __high2half2(sr) : __low2half2(sr), m2 = (v & 1) ? __high2half2(mr) : __low2half2(mr);
-                        const uint4 o = make_uint4(as_u32(__hfma2(as_h2(code_pair<0, 8>(w, w8)), s2, m2)),
-                                                   as_u32(__hfma2(as_h2(code_pair<1, 8>(w, w8)), s2, m2)),
-                                                   as_u32(__hfma2(as_h2(code_pair<2, 8>(w, w8)), s2, m2)),
-                                                   as_u32(__hfma2(as_h2(code_pair<3, 8>(w, w8)), s2, m2)));
-                        sts_u4(at + to[e] + uint32_t((v >> 1) * 16 + (v & 1) * 8) * 128, o);
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t w = (e == 0) == !swap ? w0 : w1, w8 = w >> 8;
+                            // its group of the block: column 64 half + 32 (word)
+                            const int p0 = (64 * half) / kGrp, p1 = (64 * half + 32) / kGrp;
+                            const bool second = (e == 1) != swap;
+                            const __half2 sr = p0 == p1 ? sv[p0] : second ? sv[p1] : sv[p0];
+                            const __half2 mr = p0 == p1 ? mv[p0] : second ? mv[p1] : mv[p0];
+                            const __half2 s2 = v ? __high2half2(sr) : __low2half2(sr), m2 = v ? __high2half2(mr) : __low2half2(mr);
+                            const uint4 o = make_uint4(as_u32(__hfma2(as_h2(code_pair<0, 8>(w, w8)), s2, m2)),
+                                                       as_u32(__hfma2(as_h2(code_pair<1, 8>(w, w8)), s2, m2)),
+                                                       as_u32(__hfma2(as_h2(code_pair<2, 8>(w, w8)), s2, m2)),
+                                                       as_u32(__hfma2(as_h2(code_pair<3, 8>(w, w8)), s2, m2)));
+                            sts_u4(at + to[e] + uint32_t(v * 8) * 128, o);
+                        }
                     }
+                    if (half == kAtOnce - 1 || half == 1) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&full[held]);
+                            if (held != s) mbar_arrive(&full[s]);
+                        }
+                    }
+                    if (++s == a.stages) s = 0, ph ^= 1;
+                    if (half == kAtOnce - 1) held = s;
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full_w[s]);
-                if (++s == a.stages) s = 0, ph ^= 1;
+                for (int skip = 0; skip < 2 * (kStep - 1); ++skip)
+                    if (++s == a.stages) s = 0, ph ^= 1;
             }
         }
         if (a.early) grid_dependency_wait();       // y may still be in use by the previous kernel
@@ -235,8 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         ok = __all_sync(0xffffffffu, ok);
         fence_after();
         if (ok) {
-            const int lq = warp & 3, hi = dw >> 2, half = H == 2 ? hi : 0;
-            const int c0 = H == 2 ? 0 : hi * ((a.bt / 2 + 31) / 32 * 32), c1 = H == 2 || hi ? a.bt : min(a.bt, (a.bt / 2 + 31) / 32 * 32);
+            // TMEM lanes 32 lq .. are this warp's (its number modulo 4 says which); the warps that share them and their half of the
+            // rows take a part of the tokens each
+            constexpr int kParts = kDecodeWarps / (4 * H);
+            const int lq = warp & 3, half = H == 2 ? (warp - 2) >> 3 : 0, part = (warp - 2) >> 2 & (kParts - 1);
+            const int cut = (a.bt / kParts + 31) / 32 * 32, c0 = part * cut, c1 = min(a.bt, c0 + cut);
             const int64_t n = n0 + half * kRowsM + lq * 32 + lane;
             const bool pairs = (a.N & 1) == 0 && !a.part;
             for (int c = c0; c < c1; c += 32) {
@@ -290,9 +303,9 @@ Plan plan_of(const tern_nib_weight& w, int64_t M) {
     Plan best{};
     double least = 1e30;
     for (int h = 1; h <= 2; ++h)
-        for (int bt = 16; bt <= 256; bt += 16) {
-            if (bt < 256 && bt < 128 && bt < M) continue;                // few tokens: all in one tile
-            if (bt >= 32 && int64_t(bt - 16) >= M) break;
+        for (int bt = 32; bt <= 256; bt += 16) {
+            // few tokens in one tile; many in tiles of 128 or 256 (between, the MMAs run slower: 240 200 us where 256 took 169)
+            if (M > bt ? bt % 128 != 0 : bt - 16 >= M && bt > 32) continue;
             for (int slices = 1; slices <= 8 && slices <= KB; slices *= 2) {
                 const int slice = (KB + slices - 1) / slices, real = (KB + slice - 1) / slice;
                 const int64_t rows = (w.N + kRowsM * h - 1) / (kRowsM * h), toks = (M + bt - 1) / bt;
