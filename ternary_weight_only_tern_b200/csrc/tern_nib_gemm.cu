@@ -4,16 +4,20 @@
 // A CTA computes 128 H weight rows x BT tokens: H tcgen05.mma (kind::f16, M = 128, N = BT, K = 16) per 16 columns of K
 // with the weights as A and the tokens as B, fp32 accumulators in H 256 columns of TMEM. Weights as rows: the few
 // tokens of a small batch cost few columns, and the layout's 16-byte vectors (32 codes of a row) fit the rows.
+// K goes by stages of 128 columns (H = 1) or 64 (H = 2).
 //  * warp 0, one thread: TMA loads of the x tile (BT x 64 fp16, 128-byte swizzle) into the stages;
-//  * warp 1, one thread: issues the MMAs and commits each stage back;
-//  * warps 2-9: decode. A lane loads its vectors and scales of the next 128 columns while it works on these, two stages of 64:
-//    eight codes are five integer and four fp16 operations, w = rn16(mu + s (c - 8)) four more, and leave as one 16-byte
-//    store. Rows of odd index store the other half's word first, so that a quarter warp's stores hit all banks
-//    once. The same warps bring the accumulators out of TMEM.
+//  * warp 1: issues the MMAs and commits each stage back;
+//  * warps 2-17: decode, 16 or 32 rows of a stage each, in groups that take the stages in turn. A lane loads its vectors and
+//    scales of its next stage while it works on this one: eight codes are five integer and four fp16 operations,
+//    w = rn16(mu + s (c - 8)) four more, and leave as one 16-byte store. Rows of odd index store the other half's word first,
+//    so that a quarter warp's stores hit all banks once. The same warps bring the accumulators out of TMEM.
+// With few tokens a stage costs its hand-overs (waits, proxy fence, arrivals) more than its MMAs or decoding, hence the
+// wide stages and two strips per warp.
 // Tile and slices of K are chosen per call by a cost of both sides (plan_of): waves of CTAs times the slower of the MMAs and the
 // decoding. The slices' sums go to the workspace in fp32 and are added in order by a second kernel.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "tern_nib.cuh"
 
@@ -30,11 +34,11 @@ using namespace nib;
 
 constexpr int kDecodeWarps = 16;
 constexpr int kThreads = (2 + kDecodeWarps) * 32;
-constexpr int kAhead = 2;                  // blocks of 128 columns that a decoding lane loads ahead of its own
 constexpr int kMaxStages = 6;
 constexpr int kRowsM = 128;                // rows of an MMA
-constexpr int kBK = 64;
+constexpr int kBK = 64;                    // columns of a swizzled tile
 constexpr int kABytes = kRowsM * kBK * 2;
+constexpr int kBKs(int H) { return H == 1 ? 2 : 1; }               // tiles of a stage
 constexpr int kSmemMax = 227 * 1024;
 
 struct Args {
@@ -90,20 +94,24 @@ __device__ __forceinline__ void load_tmem32(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-template <int kGrp, int H>
+// kStrips: strips that a decoding warp takes of a stage. The groups of warps that take the stages in turn, kSets, are at most
+// as many as the stages: a group's wait for a stage then follows one that says the stage's last use but one is over, so
+// that a barrier's parity is never a whole turn behind.
+template <int kGrp, int H, int kStrips>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const Args a) {
-    constexpr int per = kGroup / kGrp;                   // groups of a block
+    constexpr int per = kGroup / kGrp, kTiles = kBKs(H);  // groups of a block; tiles of a stage
+    constexpr int kSets = kDecodeWarps * kStrips / (8 * H);  // groups of decoding warps (the caller: stages >= kSets)
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t tmem_slot;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t n0 = int64_t(blockIdx.x) * kRowsM * H, m0 = int64_t(blockIdx.y) * a.bt;
-    const int kb0 = int(blockIdx.z) * a.slice, nb = min(a.slice, a.KB - kb0), steps = 2 * nb;
+    const int kb0 = int(blockIdx.z) * a.slice, nb = min(a.slice, a.KB - kb0), steps = nb * 2 / kTiles;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(&full[s], 8 * H + 1);     // the decoding warps and x's loader
+            mbar_init(&full[s], 8 * H / kStrips + 1);     // the decoding warps and x's loader
             mbar_init(&empty[s], 1);
         }
         mbar_init(&done, 1);
@@ -127,8 +135,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int i = 0, s = 0, ph = 1; i < steps; ++i) {
                 if (i >= a.stages) ok = mbar_wait(&empty[s], ph);
                 if (!ok) break;
-                mbar_arrive_expect_tx(&full[s], uint32_t(a.bt * kBK * 2));
-                tma_load_2d(smem + s * a.stage_bytes + H * kABytes, &tmap_x, (kb0 * 2 + i) * kBK, int(m0), &full[s]);
+                mbar_arrive_expect_tx(&full[s], uint32_t(kTiles * a.bt * kBK * 2));
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+                    tma_load_2d(smem + s * a.stage_bytes + kTiles * H * kABytes + j * a.bt * kBK * 2, &tmap_x, (kb0 * 2 + i * kTiles + j) * kBK,
+                                int(m0), &full[s]);
                 issued = i + 1;
                 if (++s == a.stages) s = 0, ph ^= 1;
             }
@@ -144,100 +155,105 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             if (!ok) break;
             fence_after();
             const uint32_t at = at0 + s * a.stage_bytes;
-            const uint64_t wd = matrix_desc(at), xd = matrix_desc(at + H * kABytes);      // + 2: 32 bytes on
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
+            for (int j = 0; j < kTiles; ++j) {
+                const uint64_t wd = matrix_desc(at + j * H * kABytes), xd = matrix_desc(at + kTiles * H * kABytes + j * a.bt * kBK * 2);   // + 2: 32 bytes on
 #pragma unroll
-                for (int h = 0; h < H; ++h) mma_f16(d + 256 * h, wd + (h * kABytes >> 4) + 2 * k, xd + 2 * k, idesc, i > 0 || k > 0);
+                for (int k = 0; k < kBK / 16; ++k)
+#pragma unroll
+                    for (int h = 0; h < H; ++h) mma_f16(d + 256 * h, wd + (h * kABytes >> 4) + 2 * k, xd + 2 * k, idesc, i > 0 || j > 0 || k > 0);
+            }
             commit(empty_at + s * 8);
             if (++s == a.stages) s = 0, ph ^= 1;
         }
         commit(smem_u32(&done));          // also after a timeout: every issued MMA retires first
         if (!mbar_wait(&done, 0)) ok = false;
     } else {
-        // ---- decode: a strip of the tile per warp, every block of 128 columns or (H = 1) every other; vector v: rows
-        // 8 v + g. With one MMA per step two stages are filled at a time, so that the proxy fence and the hand-over, which take
-        // longer than the decoding, are paid once for both.
-        constexpr int kStep = 2 / H, kAtOnce = H == 1 ? 2 : 1;
-        const int dw = (warp - 2) % (8 * H), first = (warp - 2) / (8 * H), g = lane >> 2, q = lane & 3;
-        const int64_t strip = min(n0 / 16 + dw, int64_t(a.strips) - 1), blk = strip * a.KB + kb0;
-        const uint4* from = reinterpret_cast<const uint4*>(a.codes + blk * kBlockWords) + lane;
-        const __half2* sc = reinterpret_cast<const __half2*>(a.scale + blk * per * 16) + g;
-        const __half2* mu = a.mu ? reinterpret_cast<const __half2*>(a.mu + blk * per * 16) + g : nullptr;
+        // ---- decode: kStrips strips of every kSets-th stage; vector 2 h + v: strip h, rows 8 v + g
+        constexpr int kWords = 2 * kTiles, kGrps = kWords * 32 > kGrp ? kWords * 32 / kGrp : 1;   // a vector's words and groups in a stage
+        const int dw = (warp - 2) % (8 * H / kStrips), set = (warp - 2) / (8 * H / kStrips), g = lane >> 2, q = lane & 3;
+        const uint32_t* from[kStrips];
+        const __half2* sc[kStrips];
+        const __half2* mu[kStrips];
+#pragma unroll
+        for (int h = 0; h < kStrips; ++h) {
+            const int64_t strip = min(n0 / 16 + dw * kStrips + h, int64_t(a.strips) - 1), blk = strip * a.KB + kb0;
+            from[h] = a.codes + blk * kBlockWords + lane * 4;
+            sc[h] = reinterpret_cast<const __half2*>(a.scale + blk * per * 16) + g;
+            mu[h] = a.mu ? reinterpret_cast<const __half2*>(a.mu + blk * per * 16) + g : nullptr;
+        }
         if (!a.early) grid_dependency_wait();
-        uint4 next[kAhead][2];
-        __half2 sn[kAhead][per], mn[kAhead][per];
-        auto load = [&](int at, int kb) {
+        uint32_t next[kStrips * 2][kWords];
+        __half2 sn[kStrips][kGrps], mn[kStrips][kGrps];
+        auto load = [&](int i) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) next[at][v] = __ldg(from + kb * (kBlockWords / 4) + 32 * v);
+            for (int h = 0; h < kStrips; ++h) {
 #pragma unroll
-            for (int p = 0; p < per; ++p) {
-                sn[at][p] = __ldg(sc + (kb * per + p) * 8);
-                if (a.mu) mn[at][p] = __ldg(mu + (kb * per + p) * 8);
+                for (int v = 0; v < 2; ++v) {
+                    if constexpr (kTiles == 2) {
+                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(from[h] + i * kBlockWords + 128 * v));
+                        next[2 * h + v][0] = u.x, next[2 * h + v][1] = u.y, next[2 * h + v][2] = u.z, next[2 * h + v][3] = u.w;
+                    } else {
+                        const uint2 u = __ldg(reinterpret_cast<const uint2*>(from[h] + (i >> 1) * kBlockWords + 128 * v + 2 * (i & 1)));
+                        next[2 * h + v][0] = u.x, next[2 * h + v][1] = u.y;
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < kGrps; ++p) {
+                    const int at = (kTiles == 2 ? i * per : (i >> 1) * per + (i & 1) * 64 / kGrp) + p;
+                    sn[h][p] = __ldg(sc[h] + at * 8);
+                    mn[h][p] = a.mu ? __ldg(mu[h] + at * 8) : __half2half2(__float2half_rn(0.f));
+                }
             }
         };
         const bool swap = g & 1;
-        uint32_t to[2];             // of the lane's two chunks (words 0 and 1 of a stage), row 16 dw + g of the tile
+        uint32_t to[2];             // of the lane's two chunks (words 0 and 1 of a tile), row 16 kStrips dw + g
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int chunk = 4 * (swap ? 1 - e : e) + q;
-            to[e] = uint32_t(16 * dw + g) * 128 + uint32_t((chunk ^ g) << 4);
+            to[e] = base + uint32_t(16 * kStrips * dw + g) * 128 + uint32_t((chunk ^ g) << 4);
         }
+        if (set < steps) load(set);
+        int s = set % a.stages, ph = 1 ^ (set / a.stages & 1);
+        for (int i = set; i < steps; i += kSets) {
+            uint32_t cur[kStrips * 2][kWords];
+            __half2 sv[kStrips][kGrps], mv[kStrips][kGrps];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (first + i * kStep < nb) load(i, first + i * kStep);
-        int s = 2 * first % a.stages, ph = 1 ^ (2 * first / a.stages & 1);
-        for (int kbase = first; kbase < nb && ok; kbase += kAhead * kStep) {
+            for (int v = 0; v < kStrips * 2; ++v)
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int kb = kbase + i * kStep;
-                if (kb >= nb || !ok) break;
-                uint4 cur[2] = {next[i][0], next[i][1]};
-                __half2 sv[per], mv[per];
+                for (int w = 0; w < kWords; ++w) cur[v][w] = next[v][w];
 #pragma unroll
-                for (int p = 0; p < per; ++p) {
-                    sv[p] = sn[i][p];
-                    mv[p] = a.mu ? mn[i][p] : __half2half2(__float2half_rn(0.f));
-                }
-                if (kb + kAhead * kStep < nb) load(i, kb + kAhead * kStep);
-                int held = s;       // the first stage not yet handed over
+            for (int h = 0; h < kStrips; ++h)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (2 * kb + half >= a.stages) ok = ok && mbar_wait(&empty[s], ph);
-                    const uint32_t at = base + s * a.stage_bytes;
+                for (int p = 0; p < kGrps; ++p) sv[h][p] = sn[h][p], mv[h][p] = mn[h][p];
+            if (i + kSets < steps) load(i + kSets);
+            if (i >= a.stages) ok = mbar_wait(&empty[s], ph);
+            if (!ok) break;
+            const uint32_t off = s * a.stage_bytes;
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const uint32_t w0 = half ? cur[v].z : cur[v].x, w1 = half ? cur[v].w : cur[v].y;
+            for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t w = (e == 0) == !swap ? w0 : w1, w8 = w >> 8;
-                            // its group of the block: column 64 half + 32 (word)
-                            const int p0 = (64 * half) / kGrp, p1 = (64 * half + 32) / kGrp;
-                            const bool second = (e == 1) != swap;
-                            const __half2 sr = p0 == p1 ? sv[p0] : second ? sv[p1] : sv[p0];
-                            const __half2 mr = p0 == p1 ? mv[p0] : second ? mv[p1] : mv[p0];
-                            const __half2 s2 = v ? __high2half2(sr) : __low2half2(sr), m2 = v ? __high2half2(mr) : __low2half2(mr);
-                            const uint4 o = make_uint4(as_u32(__hfma2(as_h2(code_pair<0, 8>(w, w8)), s2, m2)),
-                                                       as_u32(__hfma2(as_h2(code_pair<1, 8>(w, w8)), s2, m2)),
-                                                       as_u32(__hfma2(as_h2(code_pair<2, 8>(w, w8)), s2, m2)),
-                                                       as_u32(__hfma2(as_h2(code_pair<3, 8>(w, w8)), s2, m2)));
-                            sts_u4(at + to[e] + uint32_t(v * 8) * 128, o);
-                        }
+                for (int v = 0; v < kStrips * 2; ++v)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w = (e == 0) == !swap ? cur[v][2 * j] : cur[v][2 * j + 1], w8 = w >> 8;
+                        // its group of the stage: column 64 j + 32 (word)
+                        constexpr int kLast = kGrps - 1;
+                        const int p0 = min(64 * j / kGrp, kLast), p1 = min((64 * j + 32) / kGrp, kLast);
+                        const bool second = (e == 1) != swap;
+                        const __half2 sr = p0 == p1 ? sv[v >> 1][p0] : second ? sv[v >> 1][p1] : sv[v >> 1][p0];
+                        const __half2 mr = p0 == p1 ? mv[v >> 1][p0] : second ? mv[v >> 1][p1] : mv[v >> 1][p0];
+                        const __half2 s2 = v & 1 ? __high2half2(sr) : __low2half2(sr), m2 = v & 1 ? __high2half2(mr) : __low2half2(mr);
+                        const uint4 o = make_uint4(as_u32(__hfma2(as_h2(code_pair<0, 8>(w, w8)), s2, m2)),
+                                                   as_u32(__hfma2(as_h2(code_pair<1, 8>(w, w8)), s2, m2)),
+                                                   as_u32(__hfma2(as_h2(code_pair<2, 8>(w, w8)), s2, m2)),
+                                                   as_u32(__hfma2(as_h2(code_pair<3, 8>(w, w8)), s2, m2)));
+                        sts_u4(off + to[e] + uint32_t(j * H * kABytes + v * 8 * 128), o);
                     }
-                    if (half == kAtOnce - 1 || half == 1) {
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&full[held]);
-                            if (held != s) mbar_arrive(&full[s]);
-                        }
-                    }
-                    if (++s == a.stages) s = 0, ph ^= 1;
-                    if (half == kAtOnce - 1) held = s;
-                }
-                for (int skip = 0; skip < 2 * (kStep - 1); ++skip)
-                    if (++s == a.stages) s = 0, ph ^= 1;
-            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+            for (s += kSets; s >= a.stages; s -= a.stages) ph ^= 1;
         }
         if (a.early) grid_dependency_wait();       // y may still be in use by the previous kernel
         // ---- epilogue
@@ -294,9 +310,9 @@ struct Plan {
     int h, bt, slices, slice, stages, stage_bytes;
 };
 
-// Cycles of a call on the SMs: waves of CTAs, each 64 columns of K as long as the slower of its MMAs (2 bt per 128 rows) and
-// its decoding (about 260 per 128 rows), about 3000 for a CTA's start and end; slices of K add a kernel and their sums' way
-// through memory.
+// Cycles of a call on the SMs: waves of CTAs, each 64 columns of K as long as measured for the slower of its MMAs and its
+// decoding (M = 2048, 12288 x 4096: 1400 with 256 rows and tokens, 815 with 128 rows; 64 tokens: 415, decoding), about 3000 for
+// a CTA's start and end; slices of K add a kernel and their sums' way through memory.
 Plan plan_of(const tern_nib_weight& w, int64_t M) {
     const int KB = int(w.K / kGroup);
     const int64_t sms = sm_count();
@@ -310,7 +326,7 @@ Plan plan_of(const tern_nib_weight& w, int64_t M) {
                 const int slice = (KB + slices - 1) / slices, real = (KB + slice - 1) / slice;
                 const int64_t rows = (w.N + kRowsM * h - 1) / (kRowsM * h), toks = (M + bt - 1) / bt;
                 const int64_t waves = (rows * toks * real + sms - 1) / sms;
-                double c = double(waves) * (2.0 * slice * h * std::max(2.0 * bt, 260.0) + 3000.0);
+                double c = double(waves) * (2.0 * slice * (h == 1 ? std::max(3.1 * bt, 400.0) : std::max(5.4 * bt, 750.0)) + 3000.0);
                 if (real > 1) c += 4000.0 + 8.0 * double(real) * double(M) * double(w.N) / (30.0 * double(sms));
                 if (c < least) {
                     least = c;
@@ -318,12 +334,12 @@ Plan plan_of(const tern_nib_weight& w, int64_t M) {
                 }
             }
         }
-    best.stage_bytes = best.h * kABytes + best.bt * kBK * 2;
+    best.stage_bytes = kBKs(best.h) * (best.h * kABytes + best.bt * kBK * 2);
     best.stages = std::min(kMaxStages, (kSmemMax - 2048) / best.stage_bytes);
     return best;
 }
 
-template <int kGrp, int H>
+template <int kGrp, int H, int kStrips>
 tern_status launch(const Plan& p, const tern_nib_weight& w, const CUtensorMap& map, Args& a, cudaStream_t stream) {
     static std::mutex mu;
     static bool configured[64] = {false};
@@ -332,7 +348,7 @@ tern_status launch(const Plan& p, const tern_nib_weight& w, const CUtensorMap& m
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!configured[dev]) {
-            if (cudaFuncSetAttribute(gemm_kernel<kGrp, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 1024) != cudaSuccess)
+            if (cudaFuncSetAttribute(gemm_kernel<kGrp, H, kStrips>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 1024) != cudaSuccess)
                 return TERN_ERR_CUDA;
             configured[dev] = true;
         }
@@ -349,7 +365,7 @@ tern_status launch(const Plan& p, const tern_nib_weight& w, const CUtensorMap& m
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_kernel<kGrp, H>, map, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<kGrp, H, kStrips>, map, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
 }  // namespace
@@ -389,9 +405,15 @@ tern_status gemm_launch(const tern_nib_weight& w, const __half* x, int64_t M, __
     a.stage_bytes = p.stage_bytes;
     a.early = (w.flags & TERN_WEIGHT_STATIC) != 0;
     a.status = async_status_word();
-    tern_status st;
-    if (p.h == 1) st = w.group == 32 ? launch<32, 1>(p, w, map, a, stream) : w.group == 64 ? launch<64, 1>(p, w, map, a, stream) : launch<128, 1>(p, w, map, a, stream);
-    else st = w.group == 32 ? launch<32, 2>(p, w, map, a, stream) : w.group == 64 ? launch<64, 2>(p, w, map, a, stream) : launch<128, 2>(p, w, map, a, stream);
+    auto by_group = [&](auto h, auto strips) {
+        constexpr int H = decltype(h)::value, S = decltype(strips)::value;
+        return w.group == 32 ? launch<32, H, S>(p, w, map, a, stream) : w.group == 64 ? launch<64, H, S>(p, w, map, a, stream)
+                                                                                     : launch<128, H, S>(p, w, map, a, stream);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    // two strips per warp make four sets of warps with 128 rows (two with 256): as many stages have to fit
+    const tern_status st = p.stages < 2 ? TERN_ERR_SHAPE : p.h == 2 ? by_group(Two{}, Two{}) : p.stages >= 4 ? by_group(One{}, Two{}) : by_group(One{}, One{});
     if (st != TERN_OK || p.slices == 1) return st;
     cudaError_t err;
     add_slices(a.part, p.slices, M * w.N, y, stream, err);
