@@ -1,8 +1,13 @@
 // The 4-bit KV cache: quantising new keys and values into pages, and reading them back.
 //
-// Per 64 entries of a head: s = rn16((max - min) / 15), z = rn16(min), c = rint((x - z) / s). One warp takes a token of
-// one kv head: lane i holds entries (D / 32) i .. , the range is taken over the lanes of a group, and the
-// codes go to their places in the block of 16 tokens (tern.h).
+// Per 64 entries of a head: s = rn16((max - min) / 15), z = rn16(min), c = rint((x - z) / s). Bound by HBM (a call moves each
+// value once as fp16 and once in 4 bits), for long prompts about as much by the instructions of the quantising.
+//
+// One warp takes the 16 tokens of a block and kv head that are new (or asked for): lane 4 g + q holds, of tokens g and
+// g + 8, entries 32 j + 8 q .. + 7, in 16-byte loads that read 64 consecutive bytes of a token per quad, and these
+// eight codes are one word of the K layout: 512 consecutive bytes leave per warp and store. V's words hold two tokens of
+// an entry: the eight lanes 8 q .. 8 q + 7 transpose their 8 x 8 codes (three exchanges), and lane 8 q + c then
+// stores what belongs to lane 4 c + q. Where tokens of a block are not new, V's half words are stored one by one.
 #include "tern_cache.cuh"
 
 namespace tern {
@@ -17,82 +22,92 @@ struct Args {
     const int32_t* start;
     const int32_t* counts;
     int64_t B, T;
+    int64_t blocks;         // of 16 tokens that T tokens can touch
 };
 
-// The warp's token t of sequence b and head h, with its place: false past the batch.
-__device__ __forceinline__ bool token_of(const Args& a, int64_t& b, int64_t& t, int& h) {
+// The warp's block of a call: tokens pos0 + r, r < 16, of sequence b and kv head h; token t = off + r of the call.
+struct Where {
+    int64_t b, pos0, off;
+    int h;
+};
+
+__device__ __forceinline__ bool where(const Args& a, Where& w) {
     int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    h = int(i % a.pool.heads);
+    w.h = int(i % a.pool.heads);
     i /= a.pool.heads;
-    t = i % a.T;
-    b = i / a.T;
-    return b < a.B;
+    const int64_t nth = i % a.blocks;
+    w.b = i / a.blocks;
+    if (w.b >= a.B) return false;
+    const int64_t start = __ldg(a.start + w.b);
+    w.pos0 = ((start >> 4) + nth) * kTok;      // (rounds down for a negative start too)
+    w.off = w.pos0 - start;
+    return w.off < a.T;
 }
 
-template <int D>
-__device__ __forceinline__ void quantise_to(const __half* __restrict__ src, uint8_t* unit, int r, bool is_v) {
-    constexpr int E = D / 32;            // entries of a lane
+// 8 x 8 codes: lane r of eight holds row r (nibble c: column c); afterwards column r (nibble c: row c).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     const int lane = threadIdx.x & 31;
-    float f[E];
-    float lo = INFINITY, hi = -INFINITY;
-    bool odd = false;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        f[e] = __half2float(src[lane * E + e]);
-        lo = fminf(lo, f[e]);
-        hi = fmaxf(hi, f[e]);
-        odd |= !(fabsf(f[e]) < INFINITY);
-    }
-#pragma unroll
-    for (int o = 1; o < kGrp / E; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        odd |= __shfl_xor_sync(0xffffffffu, int(odd), o) != 0;
-    }
-    __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-    const __half zh = __float2half_rn(lo);
-    if (odd) sh = __ushort_as_half(0x7FFFu);
-    const float s = __half2float(sh), z = __half2float(zh), inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-    uint32_t c[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) c[e] = s > 0.f ? uint32_t(code_of(f[e], z, s, inv, 0)) : 0u;
-    const int grp = lane * E / kGrp;
-    if (!is_v) {
-        // words of 8 entries: column i at nibble i / 2 + 4 (i % 2); 8 / E lanes share a word
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int i = (lane * E + e) & 7;
-            w |= c[e] << (4 * (i / 2 + 4 * (i & 1)));
-        }
-#pragma unroll
-        for (int o = 1; o < 8 / E; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
-        if ((lane * E) % 8 == 0) {
-            const int j = lane * E / 32, q = lane * E / 8 % 4;
-            reinterpret_cast<uint32_t*>(unit)[(r * 4 + q) * (D / 32) + j] = w;
-        }
-        if ((lane * E) % kGrp == 0) {
-            __half* at = reinterpret_cast<__half*>(unit + k_scales(D)) + (r * (D / kGrp) + grp) * 2;
-            at[0] = sh;
-            at[1] = zh;
-        }
+    uint32_t o = __shfl_xor_sync(0xffffffffu, v, 4);
+    v = lane & 4 ? prmt(o, v, 0x7632) : prmt(v, o, 0x5410);                 // halves
+    o = __shfl_xor_sync(0xffffffffu, v, 2);
+    v = lane & 2 ? prmt(o, v, 0x7351) : prmt(v, o, 0x6240);                 // bytes
+    o = __shfl_xor_sync(0xffffffffu, v, 1);
+    return lane & 1 ? (v & 0xF0F0F0F0u) | (o >> 4 & 0x0F0F0F0Fu) : (v & 0x0F0F0F0Fu) | (o & 0x0F0F0F0Fu) << 4;
+}
+
+// Nibble order of a word of eight neighbouring columns (i at i / 2 + 4 (i % 2)) to the plain one, and back.
+__device__ __forceinline__ uint32_t plain_order(uint32_t w) {
+    // nibbles 0 2 4 6 | 1 3 5 7 -> 0 .. 7
+    uint32_t lo = w & 0xFFFFu, hi = w >> 16;
+    lo = (lo | lo << 8) & 0x00FF00FFu, hi = (hi | hi << 8) & 0x00FF00FFu;
+    lo = (lo | lo << 4) & 0x0F0F0F0Fu, hi = (hi | hi << 4) & 0x0F0F0F0Fu;
+    return lo | hi << 4;
+}
+
+__device__ __forceinline__ uint32_t pair_order(uint32_t w) {
+    uint32_t lo = w & 0x0F0F0F0Fu, hi = w >> 4 & 0x0F0F0F0Fu;
+    lo = (lo | lo >> 4) & 0x00FF00FFu, hi = (hi | hi >> 4) & 0x00FF00FFu;
+    lo = (lo | lo >> 8) & 0x0000FFFFu, hi = (hi | hi >> 8) & 0x0000FFFFu;
+    return lo | hi << 16;
+}
+
+template <int W>
+__device__ __forceinline__ void store_words(uint32_t* to, const uint32_t (&w)[W]) {
+    if constexpr (W == 4) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+}
+
+template <int W>
+__device__ __forceinline__ void fetch_words(const uint32_t* from, uint32_t (&w)[W]) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
-        // entry d of word (h, g = d % 8, q, j = d / 32): nibble 2 (d / 16 % 2) + d / 8 % 2 of the token's half word. The lane
-        // with entry d < 8 of a 32 gathers the other three.
-        const int h = r >> 3, q = (r & 7) >> 1, odd_tok = r & 1;
-        uint16_t* out = reinterpret_cast<uint16_t*>(unit + v_codes(D));
+        const uint2 v = *reinterpret_cast<const uint2*>(from);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+
+// The lane's entries of a token in codes, their steps and zeros.
+template <int D>
+__device__ __forceinline__ void quantise(const uint4 (&x)[D / 32], uint32_t (&w)[D / 32], __half (&s)[D / kGrp], __half (&z)[D / kGrp]) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int d = lane * E + e;
-            uint32_t w = c[e] << (4 * (d / 8 % 4 / 2 * 2 + d / 8 % 2));
-            w |= __shfl_xor_sync(0xffffffffu, w, 8 / E);
-            w |= __shfl_xor_sync(0xffffffffu, w, 16 / E);
-            if (d % 32 < 8) out[(((h * 8 + d % 8) * 4 + q) * (D / 32) + d / 32) * 2 + odd_tok] = uint16_t(w);
-        }
-        if ((lane * E) % kGrp == 0) {
-            __half* at = reinterpret_cast<__half*>(unit + v_scales(D)) + (q * (D / kGrp) + grp) * 8 + 2 * h + odd_tok;
-            at[0] = sh;
-            at[4] = zh;
+    for (int n = 0; n < D / kGrp; ++n) {
+        __half2 lo2 = as_h2(x[2 * n].x), hi2 = lo2;
+        take_range(x[2 * n], lo2, hi2);
+        take_range(x[2 * n + 1], lo2, hi2);
+        const float2 r = whole_range<4>(lo2, hi2);
+        s[n] = __float2half_rn(__fdiv_rn(__fsub_rn(r.y, r.x), 15.f));
+        z[n] = __float2half_rn(r.x);
+        if (!(fabsf(r.x) < INFINITY) || !(fabsf(r.y) < INFINITY)) s[n] = __ushort_as_half(0x7FFFu);
+        const float sf = __half2float(s[n]), zf = __half2float(z[n]), inv = sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;
+        float worst = 0.f;
+        w[2 * n] = codes_fast<0>(x[2 * n], zf, inv, worst);
+        w[2 * n + 1] = codes_fast<0>(x[2 * n + 1], zf, inv, worst);
+        if (!(sf > 0.f)) w[2 * n] = w[2 * n + 1] = 0u;
+        else if (worst > kNearTie) {
+            w[2 * n] = codes_exact<0>(x[2 * n], zf, sf);
+            w[2 * n + 1] = codes_exact<0>(x[2 * n + 1], zf, sf);
         }
     }
 }
@@ -100,44 +115,113 @@ __device__ __forceinline__ void quantise_to(const __half* __restrict__ src, uint
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Args a, const __half* __restrict__ k,
                                                           const __half* __restrict__ v) {
-    int64_t b, t;
-    int h;
-    if (!token_of(a, b, t, h)) return;
-    if (a.counts && t >= __ldg(a.counts + b)) return;
-    const int64_t at = int64_t(__ldg(a.start + b)) + t;
-    uint8_t* unit = at < 0 ? nullptr : a.pool.block<D>(b, h, at / kTok);
+    constexpr int W = D / 32, NG = D / kGrp;
+    Where w;
+    if (!where(a, w)) return;
+    const int64_t end = a.counts ? min(int64_t(__ldg(a.counts + w.b)), a.T) : a.T;     // tokens of the call
+    if (w.off >= end || w.pos0 < 0) return;
+    uint8_t* unit = a.pool.block<D>(w.b, w.h, w.pos0 / kTok);
     if (!unit) return;
-    const int64_t from = ((b * a.T + t) * a.pool.heads + h) * D;
-    quantise_to<D>(k + from, unit, int(at % kTok), false);
-    quantise_to<D>(v + from, unit, int(at % kTok), true);
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const bool whole = w.off >= 0 && w.off + kTok <= end;
+    const int64_t from = ((w.b * a.T + w.off) * a.pool.heads + w.h) * D, row = int64_t(a.pool.heads) * D;
+    bool mine[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t t = w.off + 8 * h + g;
+        mine[h] = t >= 0 && t < end;
+    }
+    uint4 x[2][2][W];           // K and V of the lane's two tokens, all loads under way at once
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                x[kv][h][j] = mine[h] ? __ldg(reinterpret_cast<const uint4*>((kv ? v : k) + from + (8 * h + g) * row + 32 * j + 8 * q))
+                                      : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t c[W];
+        __half s[NG], z[NG];
+        quantise<D>(x[0][h], c, s, z);
+        if (mine[h]) {
+            store_words<W>(reinterpret_cast<uint32_t*>(unit) + (h * 32 + lane) * W, c);
+            if (q < NG) {
+                const __half sq = NG == 1 || q == 0 ? s[0] : s[NG - 1], zq = NG == 1 || q == 0 ? z[0] : z[NG - 1];
+                reinterpret_cast<__half2*>(unit + k_scales(D))[(8 * h + g) * NG + q] = __halves2half2(sq, zq);
+            }
+        }
+        quantise<D>(x[1][h], c, s, z);
+        if (mine[h] && q < NG) {
+            const __half sq = NG == 1 || q == 0 ? s[0] : s[NG - 1], zq = NG == 1 || q == 0 ? z[0] : z[NG - 1];
+            __half* at = reinterpret_cast<__half*>(unit + v_scales(D)) + ((g >> 1) * NG + q) * 8 + 2 * h + (g & 1);
+            at[0] = sq;
+            at[4] = zq;
+        }
+        uint32_t o[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j] = transpose8(plain_order(c[j]));
+        // tokens 2 q' (low halves) and 2 q' + 1 (high) of q' = lane / 8, for the layout's lane 4 (lane % 8) + q'
+        uint32_t* to = reinterpret_cast<uint32_t*>(unit + v_codes(D)) + (h * 32 + 4 * (lane & 7) + (lane >> 3)) * W;
+        if (whole) {
+            store_words<W>(to, o);
+        } else {
+            const int64_t t = w.off + 8 * h + 2 * (lane >> 3);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if (t >= 0 && t < end) reinterpret_cast<uint16_t*>(to + j)[0] = uint16_t(o[j]);
+                if (t + 1 >= 0 && t + 1 < end) reinterpret_cast<uint16_t*>(to + j)[1] = uint16_t(o[j] >> 16);
+            }
+        }
+    }
+}
+
+// Eight codes (a word of eight neighbouring columns) as fp16 values z + s c.
+__device__ __forceinline__ uint4 values(uint32_t w, __half2 s, __half2 z) {
+    const uint32_t w8 = w >> 8;
+    return make_uint4(as_u32(__hfma2(as_h2(code_pair<0, 0>(w, w8)), s, z)), as_u32(__hfma2(as_h2(code_pair<1, 0>(w, w8)), s, z)),
+                      as_u32(__hfma2(as_h2(code_pair<2, 0>(w, w8)), s, z)), as_u32(__hfma2(as_h2(code_pair<3, 0>(w, w8)), s, z)));
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, __half* __restrict__ k, __half* __restrict__ v) {
-    constexpr int E = D / 32;
-    int64_t b, t;
-    int h;
-    if (!token_of(a, b, t, h)) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t at = int64_t(__ldg(a.start + b)) + t, to = ((b * a.T + t) * a.pool.heads + h) * D + lane * E;
-    const bool wanted = at >= 0 && !(a.counts && t >= __ldg(a.counts + b));
-    const uint8_t* unit = wanted ? a.pool.block<D>(b, h, at / kTok) : nullptr;
-    const int r = int(at % kTok), grp = lane * E / kGrp;
+    constexpr int W = D / 32, NG = D / kGrp;
+    Where w;
+    if (!where(a, w)) return;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int64_t end = a.counts ? min(int64_t(__ldg(a.counts + w.b)), a.T) : a.T;
+    const uint8_t* unit = w.pos0 >= 0 && w.off < end ? a.pool.block<D>(w.b, w.h, w.pos0 / kTok) : nullptr;
+    const int64_t to = ((w.b * a.T + w.off) * a.pool.heads + w.h) * D, row = int64_t(a.pool.heads) * D;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        float ko = 0.f, vo = 0.f;
+    for (int h = 0; h < 2; ++h) {
+        const int64_t t = w.off + 8 * h + g;
+        uint32_t kc[W] = {}, vc[W] = {};
+        __half2 ks[NG], vs[NG], vz[NG];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) ks[n] = vs[n] = vz[n] = __half2half2(__float2half_rn(0.f));
         if (unit) {
-            const int d = lane * E + e, i = d & 7;
-            const __half* ks = reinterpret_cast<const __half*>(unit + k_scales(D)) + (r * (D / kGrp) + grp) * 2;
-            const uint32_t kw = reinterpret_cast<const uint32_t*>(unit)[(r * 4 + d / 8 % 4) * (D / 32) + d / 32];
-            ko = __half2float(ks[1]) + __half2float(ks[0]) * float(kw >> (4 * (i / 2 + 4 * (i & 1))) & 15u);
-            const int hh = r >> 3, q = (r & 7) >> 1, odd = r & 1;
-            const __half* vs = reinterpret_cast<const __half*>(unit + v_scales(D)) + (q * (D / kGrp) + grp) * 8 + 2 * hh + odd;
-            const uint32_t vw = reinterpret_cast<const uint32_t*>(unit + v_codes(D))[((hh * 8 + d % 8) * 4 + q) * (D / 32) + d / 32];
-            vo = __half2float(vs[4]) + __half2float(vs[0]) * float(vw >> (4 * (d / 16 % 2 * 2 + d / 8 % 2) + 16 * odd) & 15u);
+            fetch_words<W>(reinterpret_cast<const uint32_t*>(unit) + (h * 32 + lane) * W, kc);
+            fetch_words<W>(reinterpret_cast<const uint32_t*>(unit + v_codes(D)) + (h * 32 + 4 * (lane & 7) + (lane >> 3)) * W, vc);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                ks[n] = reinterpret_cast<const __half2*>(unit + k_scales(D))[(8 * h + g) * NG + n];
+                const __half* at = reinterpret_cast<const __half*>(unit + v_scales(D)) + ((g >> 1) * NG + n) * 8 + 2 * h + (g & 1);
+                vs[n] = __half2half2(at[0]);
+                vz[n] = __half2half2(at[4]);
+            }
         }
-        k[to + e] = __float2half_rn(ko);
-        v[to + e] = __float2half_rn(vo);
+#pragma unroll
+        for (int j = 0; j < W; ++j) vc[j] = pair_order(transpose8(vc[j]));
+        if (t < 0 || t >= a.T) continue;
+        const bool there = unit && t < end;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const int64_t at = to + (8 * h + g) * row + 32 * j + 8 * q;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(k + at) = there ? values(kc[j], __low2half2(ks[j / 2]), __high2half2(ks[j / 2])) : none;
+            *reinterpret_cast<uint4*>(v + at) = there ? values(vc[j], vs[j / 2], vz[j / 2]) : none;
+        }
     }
 }
 
@@ -151,10 +235,12 @@ tern_status check_call(const tern_cache* c, const void* k, const void* v, int64_
     return aligned16(k) && aligned16(v) ? TERN_OK : TERN_ERR_ALIGN;
 }
 
+int64_t blocks_of(int64_t T) { return (T + kTok - 2) / kTok + 1; }
+
 bool grid_for(const tern_cache* c, int64_t B, int64_t T, unsigned& n) {
-    const int64_t blocks = (B * T * c->kv_heads * 32 + kThreads - 1) / kThreads;
-    n = unsigned(blocks);
-    return blocks <= 0x7fffffff;
+    const int64_t ctas = (B * blocks_of(T) * c->kv_heads * 32 + kThreads - 1) / kThreads;
+    n = unsigned(ctas);
+    return ctas <= 0x7fffffff;
 }
 
 }  // namespace
@@ -170,7 +256,7 @@ extern "C" tern_status tern_cache_append(const tern_cache* cache, const tern_hal
     if (st != TERN_OK || B == 0 || T == 0) return st;
     unsigned n;
     if (!grid_for(cache, B, T, n)) return TERN_ERR_SHAPE;
-    const Args a{pool_of(cache, table, width), start, counts, B, T};
+    const Args a{pool_of(cache, table, width), start, counts, B, T, blocks_of(T)};
     auto kernel = cache->head_dim == 64 ? append_kernel<64> : append_kernel<128>;
     kernel<<<n, kThreads, 0, as_cuda(stream)>>>(a, reinterpret_cast<const __half*>(k), reinterpret_cast<const __half*>(v));
     return launched();
@@ -183,7 +269,7 @@ extern "C" tern_status tern_cache_read(const tern_cache* cache, tern_half* k, te
     if (st != TERN_OK || B == 0 || T == 0) return st;
     unsigned n;
     if (!grid_for(cache, B, T, n)) return TERN_ERR_SHAPE;
-    const Args a{pool_of(cache, table, width), start, counts, B, T};
+    const Args a{pool_of(cache, table, width), start, counts, B, T, blocks_of(T)};
     auto kernel = cache->head_dim == 64 ? read_kernel<64> : read_kernel<128>;
     kernel<<<n, kThreads, 0, as_cuda(stream)>>>(a, reinterpret_cast<__half*>(k), reinterpret_cast<__half*>(v));
     return launched();

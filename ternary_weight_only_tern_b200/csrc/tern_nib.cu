@@ -64,25 +64,11 @@ __global__ void __launch_bounds__(kThreads) fit_kernel(const __half* __restrict_
     uint32_t out[4];
 #pragma unroll
     for (int j0 = 0; j0 < 4; j0 += span) {
-        float lo = INFINITY, hi = -INFINITY;
-        bool odd = false;                // a NaN or an infinity
+        __half2 lo2 = as_h2(raw[j0].x), hi2 = lo2;
 #pragma unroll
-        for (int j = j0; j < j0 + span; ++j) {
-            const __half2* h = reinterpret_cast<const __half2*>(&raw[j]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(h[i]);
-                lo = fminf(lo, fminf(f.x, f.y));
-                hi = fmaxf(hi, fmaxf(f.x, f.y));
-                odd |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            odd |= __shfl_xor_sync(0xffffffffu, int(odd), o) != 0;
-        }
+        for (int j = j0; j < j0 + span; ++j) take_range(raw[j], lo2, hi2);
+        const float2 range = whole_range<4>(lo2, hi2);
+        const float lo = range.x, hi = range.y;
         __half sh, mh = __float2half_rn(0.f);
         if (offset) {
             sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
@@ -90,21 +76,15 @@ __global__ void __launch_bounds__(kThreads) fit_kernel(const __half* __restrict_
         } else {
             sh = __float2half_rn(__fdiv_rn(fmaxf(fabsf(lo), fabsf(hi)), 7.f));
         }
-        if (odd) sh = __ushort_as_half(0x7FFFu);
+        if (!(fabsf(lo) < INFINITY) || !(fabsf(hi) < INFINITY)) sh = __ushort_as_half(0x7FFFu);
         const float s = __half2float(sh), m = __half2float(mh), inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
         const bool flat = !(s > 0.f);
+        float worst = 0.f;
 #pragma unroll
-        for (int j = j0; j < j0 + span; ++j) {
-            const __half2* h = reinterpret_cast<const __half2*>(&raw[j]);
-            uint32_t w = 0;
+        for (int j = j0; j < j0 + span; ++j) out[j] = codes_fast<8>(raw[j], m, inv, worst);
+        if (flat || worst > kNearTie) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(h[i]);
-                const uint32_t a = flat ? 8u : uint32_t(code_of(f.x, m, s, inv, 8));
-                const uint32_t b = flat ? 8u : uint32_t(code_of(f.y, m, s, inv, 8));
-                w |= a << (4 * i) | b << (16 + 4 * i);
-            }
-            out[j] = w;
+            for (int j = j0; j < j0 + span; ++j) out[j] = flat ? 0x88888888u : codes_exact<8>(raw[j], m, s);
         }
         if (p.q == 0) {
             const int64_t at = scale_at<kGrp>(p, KB, j0);

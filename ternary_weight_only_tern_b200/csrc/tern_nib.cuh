@@ -79,16 +79,62 @@ __device__ __forceinline__ void mma_1688_first(float (&d)[4], float a0, float a1
 // v = hi + lo, each a tf32 number, but for 2^-22 v.
 __device__ __forceinline__ float tf32_part(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFFE000u); }
 
-// Code of x for step s and zero z: rint((x - z) / s) + bias in 0 .. 15, the quotient rounded to fp32 first;
-// inv = 1 / s to fp32. t is within 1e-5 of that quotient for every |t| < 32, so unless it lies next to a
-// tie both round to the same integer; the division is done only there.
-__device__ __forceinline__ int code_of(float x, float z, float s, float inv, int bias) {
-    const float d = __fsub_rn(x, z);
-    float t = __fmul_rn(d, inv);
-    const float r = rintf(t);
-    if (fabsf(fabsf(__fsub_rn(t, r)) - 0.5f) < 1e-4f) t = __fdiv_rn(d, s);
-    const float c = fminf(fmaxf(rintf(t) + float(bias), 0.f), 15.f);
-    return int(c);
+// ---------------------------------------------------------------- quantising
+// Codes of eight neighbouring fp16 values for step s and zero z: rint((x - z) / s) + kBias in 0 .. 15, the quotient rounded
+// to fp32 first, column i at nibble i / 2 + 4 (i % 2).
+//
+// The quotient is taken as (x - z) inv with inv = 1 / s to fp32, off by less than 2^-18 for a quotient below 32, and
+// rounded by adding 1.5 2^23 (to nearest, ties to even), whose bits then carry the code. `worst` keeps the largest distance
+// to the integer: past kNearTie another rounding of the quotient could fall the other way, and the caller takes codes_exact.
+constexpr float kMagic = 12582912.f;       // 1.5 2^23
+constexpr float kNearTie = 0.5f - 1.f / 65536.f;
+
+template <int kBias>
+__device__ __forceinline__ uint32_t codes_fast(uint4 v, float z, float inv, float& worst) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(as_h2(u[i / 2]));
+        const float t = __fmul_rn(__fsub_rn(i & 1 ? f.y : f.x, z), inv);
+        const float m = __fadd_rn(t, kMagic + float(kBias));
+        worst = fmaxf(worst, fabsf(__fsub_rn(t, __fsub_rn(m, kMagic + float(kBias)))));
+        const int c = min(max(__float_as_int(m), 0x4B400000), 0x4B40000F);     // the code in the low bits
+        w += uint32_t(c) << (4 * (i / 2 + 4 * (i & 1)));
+    }
+    // less the upper bits of the eight, shifted as their codes are (modulo 2^32)
+    uint32_t upper = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) upper += 0x4B400000u << (4 * i);
+    return w - upper;
+}
+
+template <int kBias>
+__device__ __noinline__ uint32_t codes_exact(uint4 v, float z, float s) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w = 0;
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t pair = i < 2 ? u[0] : i < 4 ? u[1] : i < 6 ? u[2] : u[3];
+        const float x = __half2float(i & 1 ? __high2half(as_h2(pair)) : __low2half(as_h2(pair)));
+        const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, z), s)) + float(kBias), 0.f), 15.f);
+        w |= uint32_t(int(c)) << (4 * (i / 2 + 4 * (i & 1)));
+    }
+    return w;
+}
+
+// Smallest and largest of values seen so far; a NaN stays.
+__device__ __forceinline__ void take_range(uint4 v, __half2& lo, __half2& hi) {
+    lo = __hmin2_nan(lo, __hmin2_nan(__hmin2_nan(as_h2(v.x), as_h2(v.y)), __hmin2_nan(as_h2(v.z), as_h2(v.w))));
+    hi = __hmax2_nan(hi, __hmax2_nan(__hmax2_nan(as_h2(v.x), as_h2(v.y)), __hmax2_nan(as_h2(v.z), as_h2(v.w))));
+}
+
+// Over the pair and the `lanes` lanes that share it (a power of two): (lo, hi) of all.
+template <int kLanes>
+__device__ __forceinline__ float2 whole_range(__half2 lo, __half2 hi) {
+    __half2 r = __halves2half2(__hmin_nan(__low2half(lo), __high2half(lo)), __hneg(__hmax_nan(__low2half(hi), __high2half(hi))));
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) r = __hmin2_nan(r, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(r), o)));
+    return make_float2(__low2float(r), -__high2float(r));
 }
 
 inline bool overlaps(const void* a, size_t abytes, const void* b, size_t bbytes) {
