@@ -3,7 +3,7 @@
 // Per 64 entries of a head: s = rn16((max - min) / 15), z = rn16(min), c = rint((x - z) / s). Bound by HBM (a call moves each
 // value once as fp16 and once in 4 bits), for long prompts about as much by the instructions of the quantising.
 //
-// One warp takes the 16 tokens of a block and kv head that are new (or asked for): lane 4 g + q holds, of tokens g and
+// One warp takes K or V of the 16 tokens of a block and kv head that are new (or asked for): lane 4 g + q holds, of tokens g and
 // g + 8, entries 32 j + 8 q .. + 7, in 16-byte loads that read 64 consecutive bytes of a token per quad, and these
 // eight codes are one word of the K layout: 512 consecutive bytes leave per warp and store. V's words hold two tokens of
 // an entry: the eight lanes 8 q .. 8 q + 7 transpose their 8 x 8 codes (three exchanges), and lane 8 q + c then
@@ -25,16 +25,19 @@ struct Args {
     int64_t blocks;         // of 16 tokens that T tokens can touch
 };
 
-// The warp's block of a call: tokens pos0 + r, r < 16, of sequence b and kv head h; token t = off + r of the call.
+// The warp's block of a call: K (kv = 0) or V of tokens pos0 + r, r < 16, of sequence b and kv head h; token t = off + r
+// of the call.
 struct Where {
     int64_t b, pos0, off;
-    int h;
+    int h, kv;
 };
 
 __device__ __forceinline__ bool where(const Args& a, Where& w) {
     int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
     w.h = int(i % a.pool.heads);
     i /= a.pool.heads;
+    w.kv = int(i & 1);
+    i >>= 1;
     const int64_t nth = i % a.blocks;
     w.b = i / a.blocks;
     if (w.b >= a.B) return false;
@@ -55,15 +58,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return lane & 1 ? (v & 0xF0F0F0F0u) | (o >> 4 & 0x0F0F0F0Fu) : (v & 0x0F0F0F0Fu) | (o & 0x0F0F0F0Fu) << 4;
 }
 
-// Nibble order of a word of eight neighbouring columns (i at i / 2 + 4 (i % 2)) to the plain one, and back.
-__device__ __forceinline__ uint32_t plain_order(uint32_t w) {
-    // nibbles 0 2 4 6 | 1 3 5 7 -> 0 .. 7
-    uint32_t lo = w & 0xFFFFu, hi = w >> 16;
-    lo = (lo | lo << 8) & 0x00FF00FFu, hi = (hi | hi << 8) & 0x00FF00FFu;
-    lo = (lo | lo << 4) & 0x0F0F0F0Fu, hi = (hi | hi << 4) & 0x0F0F0F0Fu;
-    return lo | hi << 4;
-}
-
+// The plain nibble order to that of a word of eight neighbouring columns (i at i / 2 + 4 (i % 2)).
 __device__ __forceinline__ uint32_t pair_order(uint32_t w) {
     uint32_t lo = w & 0x0F0F0F0Fu, hi = w >> 4 & 0x0F0F0F0Fu;
     lo = (lo | lo >> 4) & 0x00FF00FFu, hi = (hi | hi >> 4) & 0x00FF00FFu;
@@ -88,8 +83,8 @@ __device__ __forceinline__ void fetch_words(const uint32_t* from, uint32_t (&w)[
     }
 }
 
-// The lane's entries of a token in codes, their steps and zeros.
-template <int D>
+// The lane's entries of a token in codes (kPlain: in the plain order), their steps and zeros.
+template <int D, bool kPlain>
 __device__ __forceinline__ void quantise(const uint4 (&x)[D / 32], uint32_t (&w)[D / 32], __half (&s)[D / kGrp], __half (&z)[D / kGrp]) {
 #pragma unroll
     for (int n = 0; n < D / kGrp; ++n) {
@@ -97,18 +92,12 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[D / 32], uint32_t (&w)
         take_range(x[2 * n], lo2, hi2);
         take_range(x[2 * n + 1], lo2, hi2);
         const float2 r = whole_range<4>(lo2, hi2);
-        s[n] = __float2half_rn(__fdiv_rn(__fsub_rn(r.y, r.x), 15.f));
+        const float wide = __fsub_rn(r.y, r.x);
+        s[n] = wide < INFINITY ? __float2half_rn(divided<15>(wide)) : __ushort_as_half(0x7FFFu);   // (a NaN or an infinity among them)
         z[n] = __float2half_rn(r.x);
-        if (!(fabsf(r.x) < INFINITY) || !(fabsf(r.y) < INFINITY)) s[n] = __ushort_as_half(0x7FFFu);
-        const float sf = __half2float(s[n]), zf = __half2float(z[n]), inv = sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;
-        float worst = 0.f;
-        w[2 * n] = codes_fast<0>(x[2 * n], zf, inv, worst);
-        w[2 * n + 1] = codes_fast<0>(x[2 * n + 1], zf, inv, worst);
-        if (!(sf > 0.f)) w[2 * n] = w[2 * n + 1] = 0u;
-        else if (worst > kNearTie) {
-            w[2 * n] = codes_exact<0>(x[2 * n], zf, sf);
-            w[2 * n + 1] = codes_exact<0>(x[2 * n + 1], zf, sf);
-        }
+        const float sf = __half2float(s[n]), zf = __half2float(z[n]), inv = reciprocal(sf);
+#pragma unroll
+        for (int j = 2 * n; j < 2 * n + 2; ++j) w[j] = sf > 0.f ? codes_of<0, kPlain>(x[j], zf, sf, inv) : 0u;
     }
 }
 
@@ -116,62 +105,62 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Args a, const __half* __restrict__ k,
                                                           const __half* __restrict__ v) {
     constexpr int W = D / 32, NG = D / kGrp;
+    grid_launch_dependents();
+    grid_dependency_wait();
     Where w;
     if (!where(a, w)) return;
     const int64_t end = a.counts ? min(int64_t(__ldg(a.counts + w.b)), a.T) : a.T;     // tokens of the call
     if (w.off >= end || w.pos0 < 0) return;
-    uint8_t* unit = a.pool.block<D>(w.b, w.h, w.pos0 / kTok);
-    if (!unit) return;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const bool whole = w.off >= 0 && w.off + kTok <= end;
     const int64_t from = ((w.b * a.T + w.off) * a.pool.heads + w.h) * D, row = int64_t(a.pool.heads) * D;
-    bool mine[2];
+    const __half* src = (w.kv ? v : k) + from;
+    bool mine[2], some[2];
+    uint4 x[2][W];              // the lane's two tokens, all loads under way at once
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int64_t t = w.off + 8 * h + g;
         mine[h] = t >= 0 && t < end;
+        some[h] = w.off + 8 * h + 7 >= 0 && w.off + 8 * h < end;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            x[h][j] = mine[h] ? __ldg(reinterpret_cast<const uint4*>(src + (8 * h + g) * row + 32 * j + 8 * q)) : make_uint4(0, 0, 0, 0);
     }
-    uint4 x[2][2][W];           // K and V of the lane's two tokens, all loads under way at once
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                x[kv][h][j] = mine[h] ? __ldg(reinterpret_cast<const uint4*>((kv ? v : k) + from + (8 * h + g) * row + 32 * j + 8 * q))
-                                      : make_uint4(0, 0, 0, 0);
+    uint8_t* unit = a.pool.block<D>(w.b, w.h, w.pos0 / kTok);
+    if (!unit) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        if (!some[h]) continue;             // (the whole warp)
         uint32_t c[W];
         __half s[NG], z[NG];
-        quantise<D>(x[0][h], c, s, z);
-        if (mine[h]) {
-            store_words<W>(reinterpret_cast<uint32_t*>(unit) + (h * 32 + lane) * W, c);
-            if (q < NG) {
-                const __half sq = NG == 1 || q == 0 ? s[0] : s[NG - 1], zq = NG == 1 || q == 0 ? z[0] : z[NG - 1];
-                reinterpret_cast<__half2*>(unit + k_scales(D))[(8 * h + g) * NG + q] = __halves2half2(sq, zq);
+        if (!w.kv) {
+            quantise<D, false>(x[h], c, s, z);
+            if (mine[h]) store_words<W>(reinterpret_cast<uint32_t*>(unit) + (h * 32 + lane) * W, c);
+        } else {
+            quantise<D, true>(x[h], c, s, z);
+#pragma unroll
+            for (int j = 0; j < W; ++j) c[j] = transpose8(c[j]);
+            // tokens 2 q' (low halves) and 2 q' + 1 (high) of q' = lane / 8, for the layout's lane 4 (lane % 8) + q'
+            uint32_t* to = reinterpret_cast<uint32_t*>(unit + v_codes(D)) + (h * 32 + 4 * (lane & 7) + (lane >> 3)) * W;
+            if (whole) {
+                store_words<W>(to, c);
+            } else {
+                const int64_t t = w.off + 8 * h + 2 * (lane >> 3);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    if (t >= 0 && t < end) reinterpret_cast<uint16_t*>(to + j)[0] = uint16_t(c[j]);
+                    if (t + 1 >= 0 && t + 1 < end) reinterpret_cast<uint16_t*>(to + j)[1] = uint16_t(c[j] >> 16);
+                }
             }
         }
-        quantise<D>(x[1][h], c, s, z);
         if (mine[h] && q < NG) {
             const __half sq = NG == 1 || q == 0 ? s[0] : s[NG - 1], zq = NG == 1 || q == 0 ? z[0] : z[NG - 1];
-            __half* at = reinterpret_cast<__half*>(unit + v_scales(D)) + ((g >> 1) * NG + q) * 8 + 2 * h + (g & 1);
-            at[0] = sq;
-            at[4] = zq;
-        }
-        uint32_t o[W];
-#pragma unroll
-        for (int j = 0; j < W; ++j) o[j] = transpose8(plain_order(c[j]));
-        // tokens 2 q' (low halves) and 2 q' + 1 (high) of q' = lane / 8, for the layout's lane 4 (lane % 8) + q'
-        uint32_t* to = reinterpret_cast<uint32_t*>(unit + v_codes(D)) + (h * 32 + 4 * (lane & 7) + (lane >> 3)) * W;
-        if (whole) {
-            store_words<W>(to, o);
-        } else {
-            const int64_t t = w.off + 8 * h + 2 * (lane >> 3);
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if (t >= 0 && t < end) reinterpret_cast<uint16_t*>(to + j)[0] = uint16_t(o[j]);
-                if (t + 1 >= 0 && t + 1 < end) reinterpret_cast<uint16_t*>(to + j)[1] = uint16_t(o[j] >> 16);
+            if (!w.kv) {
+                reinterpret_cast<__half2*>(unit + k_scales(D))[(8 * h + g) * NG + q] = __halves2half2(sq, zq);
+            } else {
+                __half* at = reinterpret_cast<__half*>(unit + v_scales(D)) + ((g >> 1) * NG + q) * 8 + 2 * h + (g & 1);
+                at[0] = sq;
+                at[4] = zq;
             }
         }
     }
@@ -187,41 +176,46 @@ __device__ __forceinline__ uint4 values(uint32_t w, __half2 s, __half2 z) {
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, __half* __restrict__ k, __half* __restrict__ v) {
     constexpr int W = D / 32, NG = D / kGrp;
+    grid_launch_dependents();
+    grid_dependency_wait();
     Where w;
     if (!where(a, w)) return;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int64_t end = a.counts ? min(int64_t(__ldg(a.counts + w.b)), a.T) : a.T;
     const uint8_t* unit = w.pos0 >= 0 && w.off < end ? a.pool.block<D>(w.b, w.h, w.pos0 / kTok) : nullptr;
-    const int64_t to = ((w.b * a.T + w.off) * a.pool.heads + w.h) * D, row = int64_t(a.pool.heads) * D;
+    const int64_t row = int64_t(a.pool.heads) * D;
+    __half* to = (w.kv ? v : k) + ((w.b * a.T + w.off) * a.pool.heads + w.h) * D;
+    uint32_t c[2][W] = {};
+    __half2 s[2][NG], z[2][NG];
+    if (unit) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int place = w.kv ? 4 * (lane & 7) + (lane >> 3) : lane;      // as append stored them
+            fetch_words<W>(reinterpret_cast<const uint32_t*>(unit + (w.kv ? v_codes(D) : 0)) + (h * 32 + place) * W, c[h]);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                const __half* at = w.kv ? reinterpret_cast<const __half*>(unit + v_scales(D)) + ((g >> 1) * NG + n) * 8 + 2 * h + (g & 1)
+                                        : reinterpret_cast<const __half*>(unit + k_scales(D)) + ((8 * h + g) * NG + n) * 2;
+                s[h][n] = __half2half2(at[0]);
+                z[h][n] = __half2half2(at[w.kv ? 4 : 1]);
+            }
+        }
+        if (w.kv) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < W; ++j) c[h][j] = pair_order(transpose8(c[h][j]));
+        }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int64_t t = w.off + 8 * h + g;
-        uint32_t kc[W] = {}, vc[W] = {};
-        __half2 ks[NG], vs[NG], vz[NG];
-#pragma unroll
-        for (int n = 0; n < NG; ++n) ks[n] = vs[n] = vz[n] = __half2half2(__float2half_rn(0.f));
-        if (unit) {
-            fetch_words<W>(reinterpret_cast<const uint32_t*>(unit) + (h * 32 + lane) * W, kc);
-            fetch_words<W>(reinterpret_cast<const uint32_t*>(unit + v_codes(D)) + (h * 32 + 4 * (lane & 7) + (lane >> 3)) * W, vc);
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                ks[n] = reinterpret_cast<const __half2*>(unit + k_scales(D))[(8 * h + g) * NG + n];
-                const __half* at = reinterpret_cast<const __half*>(unit + v_scales(D)) + ((g >> 1) * NG + n) * 8 + 2 * h + (g & 1);
-                vs[n] = __half2half2(at[0]);
-                vz[n] = __half2half2(at[4]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) vc[j] = pair_order(transpose8(vc[j]));
         if (t < 0 || t >= a.T) continue;
         const bool there = unit && t < end;
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            const int64_t at = to + (8 * h + g) * row + 32 * j + 8 * q;
-            const uint4 none = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(k + at) = there ? values(kc[j], __low2half2(ks[j / 2]), __high2half2(ks[j / 2])) : none;
-            *reinterpret_cast<uint4*>(v + at) = there ? values(vc[j], vs[j / 2], vz[j / 2]) : none;
-        }
+        for (int j = 0; j < W; ++j)
+            *reinterpret_cast<uint4*>(to + (8 * h + g) * row + 32 * j + 8 * q) =
+                there ? values(c[h][j], s[h][j / 2], z[h][j / 2]) : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -238,7 +232,7 @@ tern_status check_call(const tern_cache* c, const void* k, const void* v, int64_
 int64_t blocks_of(int64_t T) { return (T + kTok - 2) / kTok + 1; }
 
 bool grid_for(const tern_cache* c, int64_t B, int64_t T, unsigned& n) {
-    const int64_t ctas = (B * blocks_of(T) * c->kv_heads * 32 + kThreads - 1) / kThreads;
+    const int64_t ctas = (B * blocks_of(T) * 2 * c->kv_heads * 32 + kThreads - 1) / kThreads;
     n = unsigned(ctas);
     return ctas <= 0x7fffffff;
 }
@@ -258,8 +252,7 @@ extern "C" tern_status tern_cache_append(const tern_cache* cache, const tern_hal
     if (!grid_for(cache, B, T, n)) return TERN_ERR_SHAPE;
     const Args a{pool_of(cache, table, width), start, counts, B, T, blocks_of(T)};
     auto kernel = cache->head_dim == 64 ? append_kernel<64> : append_kernel<128>;
-    kernel<<<n, kThreads, 0, as_cuda(stream)>>>(a, reinterpret_cast<const __half*>(k), reinterpret_cast<const __half*>(v));
-    return launched();
+    return launch_dependent(kernel, n, kThreads, as_cuda(stream), a, reinterpret_cast<const __half*>(k), reinterpret_cast<const __half*>(v));
 }
 
 extern "C" tern_status tern_cache_read(const tern_cache* cache, tern_half* k, tern_half* v, int64_t B, int64_t T,
@@ -271,6 +264,5 @@ extern "C" tern_status tern_cache_read(const tern_cache* cache, tern_half* k, te
     if (!grid_for(cache, B, T, n)) return TERN_ERR_SHAPE;
     const Args a{pool_of(cache, table, width), start, counts, B, T, blocks_of(T)};
     auto kernel = cache->head_dim == 64 ? read_kernel<64> : read_kernel<128>;
-    kernel<<<n, kThreads, 0, as_cuda(stream)>>>(a, reinterpret_cast<__half*>(k), reinterpret_cast<__half*>(v));
-    return launched();
+    return launch_dependent(kernel, n, kThreads, as_cuda(stream), a, reinterpret_cast<__half*>(k), reinterpret_cast<__half*>(v));
 }

@@ -51,6 +51,7 @@ template <int kGrp>
 __global__ void __launch_bounds__(kThreads) fit_kernel(const __half* __restrict__ W, int64_t N, int64_t K, int offset,
                                                        uint32_t* __restrict__ codes, __half* __restrict__ scale,
                                                        __half* __restrict__ mu) {
+    grid_dependency_wait();     // (and no early start for the kernel after: it may read these weights as static ones)
     const int64_t KB = K / kGroup;
     Place p;
     if (!place_of((N + 15) / 16, KB, p)) return;
@@ -69,23 +70,13 @@ __global__ void __launch_bounds__(kThreads) fit_kernel(const __half* __restrict_
         for (int j = j0; j < j0 + span; ++j) take_range(raw[j], lo2, hi2);
         const float2 range = whole_range<4>(lo2, hi2);
         const float lo = range.x, hi = range.y;
-        __half sh, mh = __float2half_rn(0.f);
-        if (offset) {
-            sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-            mh = __float2half_rn(__fadd_rn(lo, __fmul_rn(8.f, __half2float(sh))));
-        } else {
-            sh = __float2half_rn(__fdiv_rn(fmaxf(fabsf(lo), fabsf(hi)), 7.f));
-        }
-        if (!(fabsf(lo) < INFINITY) || !(fabsf(hi) < INFINITY)) sh = __ushort_as_half(0x7FFFu);
-        const float s = __half2float(sh), m = __half2float(mh), inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-        const bool flat = !(s > 0.f);
-        float worst = 0.f;
+        const float wide = offset ? __fsub_rn(hi, lo) : fmaxf(fabsf(lo), fabsf(hi));
+        __half sh = __float2half_rn(offset ? divided<15>(wide) : divided<7>(wide));
+        const __half mh = __float2half_rn(offset ? __fadd_rn(lo, __fmul_rn(8.f, __half2float(sh))) : 0.f);
+        if (!(wide < INFINITY)) sh = __ushort_as_half(0x7FFFu);       // a NaN or an infinity in the group
+        const float s = __half2float(sh), m = __half2float(mh), inv = reciprocal(s);
 #pragma unroll
-        for (int j = j0; j < j0 + span; ++j) out[j] = codes_fast<8>(raw[j], m, inv, worst);
-        if (flat || worst > kNearTie) {
-#pragma unroll
-            for (int j = j0; j < j0 + span; ++j) out[j] = flat ? 0x88888888u : codes_exact<8>(raw[j], m, s);
-        }
+        for (int j = j0; j < j0 + span; ++j) out[j] = s > 0.f ? codes_of<8>(raw[j], m, s, inv) : 0x88888888u;
         if (p.q == 0) {
             const int64_t at = scale_at<kGrp>(p, KB, j0);
             scale[at] = sh;
@@ -100,6 +91,8 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint32_t* __res
                                                            const __half* __restrict__ scale,
                                                            const __half* __restrict__ mu, int64_t N, int64_t K,
                                                            __half* __restrict__ out) {
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int64_t KB = K / kGroup;
     Place p;
     if (!place_of((N + 15) / 16, KB, p) || p.row >= N) return;
@@ -171,10 +164,8 @@ extern "C" tern_status tern_nib_fit(const tern_half* W, int64_t N, int64_t K, in
     if (!W || !codes || !scale || (offset && !mu)) return TERN_ERR_NULL;
     if (!aligned16(W) || !aligned16(codes) || !aligned16(scale) || (offset && !aligned16(mu))) return TERN_ERR_ALIGN;
     auto kernel = group == 32 ? fit_kernel<32> : group == 64 ? fit_kernel<64> : fit_kernel<128>;
-    kernel<<<blocks_for(N, K), kThreads, 0, as_cuda(stream)>>>(reinterpret_cast<const __half*>(W), N, K, offset != 0,
-                                                               codes, reinterpret_cast<__half*>(scale),
-                                                               reinterpret_cast<__half*>(mu));
-    return launched();
+    return launch_dependent(kernel, blocks_for(N, K), kThreads, as_cuda(stream), reinterpret_cast<const __half*>(W), N, K, int(offset != 0),
+                            codes, reinterpret_cast<__half*>(scale), reinterpret_cast<__half*>(mu));
 }
 
 extern "C" tern_status tern_nib_dequant(const tern_nib_weight* w, tern_half* out, tern_stream stream) {
@@ -183,10 +174,8 @@ extern "C" tern_status tern_nib_dequant(const tern_nib_weight* w, tern_half* out
     if (!out) return TERN_ERR_NULL;
     if (!aligned16(out)) return TERN_ERR_ALIGN;
     auto kernel = w->group == 32 ? dequant_kernel<32> : w->group == 64 ? dequant_kernel<64> : dequant_kernel<128>;
-    kernel<<<blocks_for(w->N, w->K), kThreads, 0, as_cuda(stream)>>>(
-        w->codes, reinterpret_cast<const __half*>(w->scale), reinterpret_cast<const __half*>(w->mu), w->N, w->K,
-        reinterpret_cast<__half*>(out));
-    return launched();
+    return launch_dependent(kernel, blocks_for(w->N, w->K), kThreads, as_cuda(stream), w->codes, reinterpret_cast<const __half*>(w->scale),
+                            reinterpret_cast<const __half*>(w->mu), w->N, w->K, reinterpret_cast<__half*>(out));
 }
 
 extern "C" tern_status tern_nib_pack(const uint8_t* c, const tern_half* s, const tern_half* m, int64_t N, int64_t K,

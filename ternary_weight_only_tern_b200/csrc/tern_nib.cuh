@@ -81,45 +81,46 @@ __device__ __forceinline__ float tf32_part(float v) { return __uint_as_float(__f
 
 // ---------------------------------------------------------------- quantising
 // Codes of eight neighbouring fp16 values for step s and zero z: rint((x - z) / s) + kBias in 0 .. 15, the quotient rounded
-// to fp32 first, column i at nibble i / 2 + 4 (i % 2).
+// to fp32 first, column i at nibble i / 2 + 4 (i % 2) (kPlain: at nibble i). inv = 1 / s to an ulp. With no bias x >= z is
+// the caller's.
 //
-// The quotient is taken as (x - z) inv with inv = 1 / s to fp32, off by less than 2^-18 for a quotient below 32, and
-// rounded by adding 1.5 2^23 (to nearest, ties to even), whose bits then carry the code. `worst` keeps the largest distance
-// to the integer: past kNearTie another rounding of the quotient could fall the other way, and the caller takes codes_exact.
-constexpr float kMagic = 12582912.f;       // 1.5 2^23
-constexpr float kNearTie = 0.5f - 1.f / 65536.f;
-
-template <int kBias>
-__device__ __forceinline__ uint32_t codes_fast(uint4 v, float z, float inv, float& worst) {
+// The quotient is q + r inv with q = (x - z) inv and the exact remainder r = (x - z) - q s, rounded once: that is off the
+// true one by less than 2^-21 ulp, and a quotient by the 11 bits of a step is at least 2^-12 ulp from every midpoint of two
+// fp32 numbers, so it is the IEEE quotient. It is rounded by adding 1.5 2^23 (to nearest, ties to even), whose bits then carry
+// the code.
+template <int kBias, bool kPlain = false>
+__device__ __forceinline__ uint32_t codes_of(uint4 v, float z, float s, float inv) {
+    constexpr float kMagic = 12582912.f + float(kBias);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t w = 0;
+    uint32_t w = 0, upper = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float2 f = __half22float2(as_h2(u[i / 2]));
-        const float t = __fmul_rn(__fsub_rn(i & 1 ? f.y : f.x, z), inv);
-        const float m = __fadd_rn(t, kMagic + float(kBias));
-        worst = fmaxf(worst, fabsf(__fsub_rn(t, __fsub_rn(m, kMagic + float(kBias)))));
-        const int c = min(max(__float_as_int(m), 0x4B400000), 0x4B40000F);     // the code in the low bits
-        w += uint32_t(c) << (4 * (i / 2 + 4 * (i & 1)));
+        const float d = __fsub_rn(i & 1 ? f.y : f.x, z), q = __fmul_rn(d, inv);
+        const float m = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, d), inv, q), kMagic);
+        int c = min(__float_as_int(m), 0x4B40000F);                 // the code in the low bits
+        if (kBias) c = max(c, 0x4B400000);
+        const int at = 4 * (kPlain ? i : i / 2 + 4 * (i & 1));
+        w += uint32_t(c) << at;
+        upper += 0x4B400000u << at;        // the upper bits, shifted as the codes are (modulo 2^32)
     }
-    // less the upper bits of the eight, shifted as their codes are (modulo 2^32)
-    uint32_t upper = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) upper += 0x4B400000u << (4 * i);
     return w - upper;
 }
 
-template <int kBias>
-__device__ __noinline__ uint32_t codes_exact(uint4 v, float z, float s) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t w = 0;
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t pair = i < 2 ? u[0] : i < 4 ? u[1] : i < 6 ? u[2] : u[3];
-        const float x = __half2float(i & 1 ? __high2half(as_h2(pair)) : __low2half(as_h2(pair)));
-        const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, z), s)) + float(kBias), 0.f), 15.f);
-        w |= uint32_t(int(c)) << (4 * (i / 2 + 4 * (i & 1)));
-    }
-    return w;
+// 1 / s to an ulp.
+__device__ __forceinline__ float reciprocal(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+
+// x / kBy as the IEEE division rounds it: a quotient by the reciprocal, and the exact remainder's share. (Checked over every
+// fp32 mantissa for 15 and 7; x is 0 or at least 2^-24, or not finite: then so is the result.)
+template <int kBy>
+__device__ __forceinline__ float divided(float x) {
+    constexpr float r = 1.f / float(kBy);
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, float(kBy), x), r, q);
 }
 
 // Smallest and largest of values seen so far; a NaN stays.
@@ -157,6 +158,21 @@ inline tern_status check_nib(const tern_nib_weight* w) {
     if (!w->codes || !w->scale) return TERN_ERR_NULL;
     if (!aligned16(w->codes) || !aligned16(w->scale) || (w->mu && !aligned16(w->mu))) return TERN_ERR_ALIGN;
     return TERN_OK;
+}
+
+// Launches a kernel that waits for the one before it itself (programmatic dependent launch).
+template <typename... P, typename... A>
+inline tern_status launch_dependent(void (*kernel)(P...), unsigned ctas, unsigned threads, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
 inline tern_status launched() { return cudaGetLastError() == cudaSuccess ? TERN_OK : TERN_ERR_CUDA; }
