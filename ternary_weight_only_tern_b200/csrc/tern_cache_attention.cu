@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
             const bool whole = have == 3u && ((v >= whole0 && v < whole1) || v < sink1);
             const uint8_t* unit = ring + slot * 2 * U;
             if (whole) {
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < 2; ++k) block_step<D, NT, false>(unit + k * U, 0, qf, qx, pos, a, st);
             } else {
                 const int j0 = seq.pair(v) * kPair;
