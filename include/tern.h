@@ -387,7 +387,7 @@ size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, 
  * tokens of each sequence, the queries' own among them (negative: none). counts int32 [B] or NULL
  * (T each): sequence b has counts[b] queries (clamped to 0 .. T), query i at token lens[b] - counts[b] +
  * i; rows of o at i >= counts[b] are left as they were. A query at token p sees token j when
- * j <= p, and, with window > 0, j > p - window or j < sinks. One that sees nothing gets zeros. Scores,
+ * j <= p, and, with window > 0, j > p - window or j < sinks. One that sees nothing gets zeros. |scale| <= 1e4. Scores,
  * softmax and sums in fp32, the probabilities rounded to fp16 for the product with V, V to fp16 once.
  * q and o must not overlap. Workspace rule and capture as for tern_linear.                */
 tern_status tern_cache_attention(const tern_cache* cache, const tern_half* q, int64_t B, int64_t T, int64_t heads,

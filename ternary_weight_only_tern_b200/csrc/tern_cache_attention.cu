@@ -40,6 +40,7 @@ constexpr int kSetup = 12;                 // what a (sequence, head, tile) cost
                                            // 102.8 with 4, 90.5 with 8, 86.1 with 12, 87.9 with 24)
 constexpr int kMinUnits = 8;               // cost per CTA at least
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMaxScale = 1e4f;          // keeps scale q k of finite inputs finite
 
 struct Desc {               // a (sequence, kv head, row tile) in pieces: where the first lies
     int b, h, rt, pieces;   // pieces < 2: nothing to join
@@ -723,7 +724,7 @@ extern "C" tern_status tern_cache_attention(const tern_cache* cache, const tern_
                                             tern_half* o, void* workspace, size_t workspace_bytes, tern_stream stream) {
     const tern_status st = check_attention(cache, B, T, heads);
     if (st != TERN_OK) return st;
-    if (!batch_ok(B, T, width) || window < 0 || sinks < 0 || !isfinite(scale)) return TERN_ERR_SHAPE;
+    if (!batch_ok(B, T, width) || window < 0 || sinks < 0 || !(fabsf(scale) <= kMaxScale)) return TERN_ERR_SHAPE;
     if (B == 0 || T == 0) return TERN_OK;
     if (!q || !o || !lens || (!table && width)) return TERN_ERR_NULL;
     if (!aligned16(q) || !aligned16(o)) return TERN_ERR_ALIGN;

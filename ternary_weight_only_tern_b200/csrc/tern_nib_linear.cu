@@ -4,8 +4,9 @@
 //   y[m, n] = sum_g s[n, g] sum_{k in g} (c[n, k] - 8) x[m, k] + mu[n, g] sum_{k in g} x[m, k].
 // The inner sums run on mma.sync m16n8k16 with a strip's 16 rows of codes plus 64, exact in fp16, as A and 8 tokens as
 // B's columns; a group's accumulators are scaled in fp32. The 72 too much and the offset, -72 s X + mu X with X = sum x
-// of the group, are a product too at groups of 32 and 64: two m16n8k8 in tf32, where s and mu are exact and X is taken
-// in two parts, per block of 128 columns (in fp32 instructions they took more issue slots than the codes). The layout
+// of the group, are four fp32 operations per group and token pair, and at group 32 a product of their own: two m16n8k8
+// in tf32 per block of 128 columns, where s and mu are exact and X is taken in two parts (65543 x 2560, 6 tokens: 24.9 us
+// against 27.6; at group 64 the plain form: 131072 x 4096, 16 tokens, 91.7 against 119.4). The layout
 // is that of A: one 16-byte shared-memory read gives a lane its four words, a word is four pairs of neighbouring
 // columns, and x is read as it lies.
 //
@@ -44,6 +45,7 @@ constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kMaxStages = 4;
 constexpr int kStageBlocks = 32;           // blocks of 128 columns in a stage at most
 constexpr int64_t kMaxM = 16;
+constexpr int kTf32Per = 4;                // groups of a block from which the correction is a tf32 product
 
 struct Args {
     const uint32_t* codes;
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const Args a) {
         const int g = lane >> 2, q = lane & 3;
         ok = mbar_wait(bars + 2 * kMaxStages + 4, 0);
         float4* sums = reinterpret_cast<float4*>(smem + a.sum_off);        // [nb per][8 NT] -72 X and X of a group, in two parts
-        float2* plain = reinterpret_cast<float2*>(smem + a.sum_off);       // or X alone, [nb][8 NT / 2], where a block is one group
+        float2* plain = reinterpret_cast<float2*>(smem + a.sum_off);       // or X alone, [nb per][8 NT / 2]
         // the lane's token of each 8 (a token past the last repeats it: its columns are never written)
         const uint8_t* xa[NT];
 #pragma unroll
@@ -156,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const Args a) {
                         mma_next(acc, one, xv.z, xv.w);
                     }
                     if (g == 0) {
-                        if constexpr (per == 1) {
-                            plain[kb * 8 * NT / 2 + 4 * t + q] = make_float2(acc[0], acc[1]);
+                        if constexpr (per != kTf32Per) {
+                            plain[(kb * per + j0 / span) * 8 * NT / 2 + 4 * t + q] = make_float2(acc[0], acc[1]);
                         } else {
                             float4* to = sums + (kb * per + j0 / span) * 8 * NT + 8 * t + 2 * q;
 #pragma unroll
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const Args a) {
                     const uint4 u = from[0], v = from[32];
                     const uint32_t wa[4] = {u.x, u.y, u.z, u.w}, wb[4] = {v.x, v.y, v.z, v.w};
                     const __half2* sc_at = reinterpret_cast<const __half2*>(ring + scale_off + b * per * 32) + g;
-                    if constexpr (per > 1) {
+                    if constexpr (per == kTf32Per) {
                         // column q of the tf32 product: group q of the block (none from `per` on)
                         float2 sq = make_float2(0.f, 0.f), mq = make_float2(0.f, 0.f);
                         if (q < per) {
@@ -227,16 +229,16 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const Args a) {
                             sum[t][2] += sc.y * acc[t][2];
                             sum[t][3] += sc.y * acc[t][3];
                         }
-                        if constexpr (per == 1) {
+                        if constexpr (per != kTf32Per) {
                             float2 mu = make_float2(-72.f * sc.x, -72.f * sc.y);
                             if (a.mu) {
-                                const float2 f = __half22float2(sc_at[(mu_off - scale_off) / 4]);
+                                const float2 f = __half22float2(sc_at[(mu_off - scale_off) / 4 + j0 / span * 8]);
                                 mu.x += f.x;
                                 mu.y += f.y;
                             }
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                const float2 X = plain[kb * 8 * NT / 2 + 4 * t + q];
+                                const float2 X = plain[(kb * per + j0 / span) * 8 * NT / 2 + 4 * t + q];
                                 sum[t][0] += mu.x * X.x;
                                 sum[t][1] += mu.x * X.y;
                                 sum[t][2] += mu.y * X.x;
@@ -341,7 +343,7 @@ bool layout(const tern_nib_weight& w, int M, Plan& p, int slices, int stages, in
     at = up(at + int64_t(M) * (int64_t(p.slice) * kGroup * 2 + 64));
     if (at > limit) return false;
     p.sum_off = int(at);
-    at = up(at + int64_t(p.slice) * per * 8 * p.nt * (per == 1 ? 4 : 16));
+    at = up(at + int64_t(p.slice) * per * 8 * p.nt * (per == kTf32Per ? 16 : 4));
     p.ring_off = int(at);
     at = up(at + int64_t(stages) * p.stage_bytes);
     p.red_off = int(at);

@@ -176,6 +176,69 @@ def test_attention_over_long_lengths(D):
     check_attention(o, q, K, V, lens, [2] * 3, D**-0.5, 0, 0)
 
 
+def test_pages_past_four_gigabytes():
+    """A pool of 4.6 GB with a sequence in its first and last pages: byte offsets past 32 bits in all three operators."""
+    rng = np.random.default_rng(12)
+    pages, page, Hk, D = 31500, 128, 8, 128
+    cache = api.PagedCache(torch.empty((pages, Hk, page // 16, 18 * D), dtype=torch.uint8, device="cuda"))
+    table = np.array([[pages - 1, 0, pages - 2]], np.int32)
+    n = 300
+    k, v = (rng.standard_normal((1, n, Hk, D)).astype(np.float16) for _ in range(2))
+    zero = cuda(np.zeros(1, np.int32))
+    api.cache_append(cache, cuda(k), cuda(v), cuda(table), zero)
+    K, V = (no.cache_values(*no.cache_quantise(x[0])) for x in (k, v))
+    got = api.cache_read(cache, cuda(table), zero, n)
+    assert np.array_equal(got[0][0].cpu().numpy(), K.astype(np.float16)) and np.array_equal(got[1][0].cpu().numpy(), V.astype(np.float16))
+    q = rng.standard_normal((1, 2, 16, D)).astype(np.float16)
+    o = api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array([n], np.int32))).cpu().numpy()
+    check_attention(o, q, [K], [V], [n], [2], D**-0.5, 0, 0)
+
+
+@pytest.mark.parametrize("B", [129, 700])
+def test_batches_past_one_scan(B):
+    """More sequences than a CTA has threads, most of them empty or tiny, one long among them."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 20, B)]
+    lens[B - 3] = 1500
+    cache, table, K, V, _, _ = make(rng, lens, 16, 1, 64)
+    q = rng.standard_normal((B, 1, 2, 64)).astype(np.float16)
+    o = api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array(lens, np.int32)), window=1000, sinks=3).cpu().numpy()
+    check_attention(o, q, K, V, lens, [1] * B, 0.125, 1000, 3)
+
+
+def test_many_heads_and_tiles():
+    """Every (sequence, head, tile) counts: more of them than CTAs, rows that do not fill a tile."""
+    rng = np.random.default_rng(33)
+    lens = [100, 37, 260]
+    cache, table, K, V, _, _ = make(rng, lens, 48, 40, 64)
+    q = rng.standard_normal((3, 7, 200, 64)).astype(np.float16)
+    o = api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array(lens, np.int32))).cpu().numpy()
+    check_attention(o, q, K, V, lens, [7] * 3, 0.125, 0, 0)
+
+
+def test_empty_calls():
+    cache = api.PagedCache.empty(2, 16, 2, 64)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f16 = lambda *s: torch.ones(s, dtype=torch.float16, device="cuda")  # noqa: E731
+    api.cache_append(cache, f16(0, 3, 2, 64), f16(0, 3, 2, 64), i32(0, 4), i32(0))
+    api.cache_append(cache, f16(2, 0, 2, 64), f16(2, 0, 2, 64), i32(2, 4), i32(2))
+    api.cache_append(cache, f16(1, 3, 2, 64), f16(1, 3, 2, 64), i32(1, 0), i32(1))        # a table without columns
+    assert not cache.pool.any()
+    assert not api.cache_read(cache, i32(1, 0), i32(1), 3)[0].any()
+    assert api.cache_attention(f16(0, 1, 4, 64), cache, i32(0, 4), i32(0)).shape == (0, 1, 4, 64)
+    assert not api.cache_attention(f16(2, 1, 4, 64), cache, i32(2, 0), i32(2) + 5).any()
+    with pytest.raises(ValueError, match="shape"):
+        api.cache_attention(f16(1, 1, 3, 64), cache, i32(1, 4), i32(1))
+    with pytest.raises(ValueError, match="rows"):
+        api.cache_attention(f16(2, 1, 4, 64), cache, i32(1, 4), i32(2))
+    with pytest.raises(ValueError, match="entries"):
+        api.cache_append(cache, f16(2, 1, 2, 64), f16(2, 1, 2, 64), i32(2, 4), i32(1))
+    with pytest.raises(TypeError, match="int32"):
+        api.cache_read(cache, i32(1, 4), torch.zeros(1, dtype=torch.int64, device="cuda"), 3)
+    with pytest.raises(ValueError, match="contiguous"):
+        api.cache_attention(f16(1, 1, 64, 4).transpose(2, 3), cache, i32(1, 4), i32(1))
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(4)
     lens = [int(n) for n in rng.integers(0, 90, 300)]

@@ -122,7 +122,7 @@ def test_attention_refusals(lib):
     assert call(B=0, q=None) == S["TERN_OK"]
     assert call(T=0, o=None) == S["TERN_OK"]
     for kw in (dict(B=-1), dict(T=65), dict(T=-1), dict(H=0), dict(H=7), dict(width=-1), dict(window=-1), dict(sinks=-1),
-               dict(scale=float("nan")), dict(scale=float("inf")), dict(o=F + 256)):
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-1.1e4), dict(o=F + 256)):
         assert call(**kw) == S["TERN_ERR_SHAPE"], kw
     for kw in (dict(q=None), dict(o=None), dict(lens=None), dict(table=None)):
         assert call(**kw) == S["TERN_ERR_NULL"], kw

@@ -139,6 +139,28 @@ def test_linear_full_sizes_on_sampled_rows(M, N, K, group):
     check_product(y[:, rows], x, no.nib_values(c[rows], s[rows], mu[rows]))
 
 
+@pytest.mark.parametrize("M,N,K,group", [(600, 4864, 512, 32), (600, 4864, 384, 64), (1000, 1000, 1024, 128), (257, 2100, 640, 32),
+                                         (128, 515, 2560, 64), (112, 4099, 256, 128), (2049, 300, 128, 32)])
+def test_linear_of_many_tokens_on_sampled_rows(M, N, K, group):
+    """Tiles of 128 and 256 rows, of 112 to 256 tokens, ragged both ways, with and without slices of K."""
+    rng = np.random.default_rng(N + M)
+    c, s, mu = draw(rng, N, K, group, True)
+    x = rng.standard_normal((M, K), dtype=np.float32).astype(np.float16)
+    y = api.nib_linear(torch.from_numpy(x).cuda(), weight(c, s, mu)).cpu().numpy()
+    rows = np.unique(np.concatenate([rng.choice(N, 150, replace=False), [0, N - 1]]))
+    check_product(y[:, rows], x, no.nib_values(c[rows], s[rows], mu[rows]))
+
+
+@pytest.mark.parametrize("M", [1, 8, 16, 40])
+def test_activations_of_one_sign_lose_nothing(M):
+    """A large common part of x: the decoding's excess, 72 times the sum of x, has to come off exactly enough."""
+    rng = np.random.default_rng(M)
+    c, s, mu = draw(rng, 300, 4096, 32, False)
+    x = (rng.standard_normal((M, 4096)) * 0.25 + 20).astype(np.float16)
+    y = api.nib_linear(torch.from_numpy(x).cuda(), weight(c, s, mu)).cpu().numpy()
+    check_product(y, x, no.nib_values(c, s, mu))
+
+
 @pytest.mark.parametrize("M", [1, 12, 40, 300])
 def test_linear_writes_its_rows_alone(M):
     """Outputs and workspace between guard words, a weight of 16 rows more than the last strip needs."""
