@@ -17,11 +17,13 @@
 // the lens itself. A CTA's four warps take the pairs of a range in turn, each through its own ring of bulk
 // copies (a block is contiguous, 18 D bytes) and with its own running maximum, sum and O^T, and join them in
 // shared memory. A (sequence, head, tile) that lies in one range is finished there; the pieces of one that
-// crosses ranges go to the workspace and a second, small kernel joins them, in the order of the ranges.
-// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 86 us (3.8 TB/s), bound
+// crosses ranges go to the workspace and a second, small kernel joins them, in the order of the ranges. Where no (sequence,
+// head, tile) can be long, by the table's width and the window, each has a CTA of its own instead.
+// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 85 us (3.9 TB/s), bound
 // by instruction issue (57 % of the slots, 337 warp instructions per block).
 #include <math.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "tern_cache.cuh"
@@ -31,8 +33,12 @@ namespace {
 
 using namespace kv;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kSplitWarps = 4;             // warps of a CTA where segments are split
+constexpr int kDirectWarps = 8;            // and where each has a CTA of its own
+constexpr int kDirectUnits = 36;           // units of a segment up to which it has (measured, 1 / 4 / 16 / 64 sequences of 8 kv heads:
+                                           // 300 tokens 6.8 6.9 8.4 15.9 us against 9.0 10.1 12.2 19.2 split; 1000 tokens
+                                           // 10.0 10.0 13.4 26.4 against 9.4 10.8 13.9 28.1; 2000 15.2 15.2 20.6 38.8
+                                           // against 9.7 12.5 16.3 37.2)
 constexpr int kPair = 2 * kTok;            // tokens of a unit of work: two blocks
 constexpr int kSlots = 2;                  // units in a warp's ring
 constexpr int kSetup = 12;                 // what a (sequence, head, tile) costs beyond its units, in units (measured: its
@@ -303,6 +309,7 @@ __device__ __forceinline__ void bulk_more(bool who, uint32_t to, const void* fro
 
 // Inclusive sum over the CTA's threads; total: over all of them. `sums` holds kWarps values and is free again
 // after the next barrier.
+template <int kWarps>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -322,7 +329,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
     return v;
 }
 
-template <int D, int NT>
+template <int D, int NT, int kWarps>
 struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kPitch = D + 1;
@@ -336,9 +343,12 @@ struct Smem {
     float m[kWarps][kRows], l[kWarps][kRows];
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(const Args a) {
-    using S = Smem<D, NT>;
+// kDirect: CTA i takes the whole of segment i, and nothing is split or joined.
+template <int D, int NT, bool kDirect>
+__global__ void __launch_bounds__((kDirect ? kDirectWarps : kSplitWarps) * 32, kDirect ? (NT == 1 ? 2 : 1) : (NT == 1 ? 4 : 3))
+    attention_kernel(const Args a) {
+    constexpr int kWarps = kDirect ? kDirectWarps : kSplitWarps, kThreads = kWarps * 32;
+    using S = Smem<D, NT, kWarps>;
     constexpr int W = D / 32, NG = D / kGrp, kRows = 8 * NT, U = unit_bytes(D);   // U: bytes of a block
     extern __shared__ __align__(128) uint8_t raw[];
     S& sm = *reinterpret_cast<S*>(raw);
@@ -352,46 +362,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
 
     // ---- this CTA's range of the cost of all (sequence, head, tile)
     const int per_seq = a.pool.heads * a.RT;
-    int64_t total = 0, mine = 0, incl = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        mine = b < a.B ? int64_t(seq_of(a, b).cost()) * per_seq : 0;
-        int64_t t;
-        incl = total + block_scan(mine, sm.sums, t);
-        total += t;
-    }
-    const int64_t quota = max((total + gridDim.x - 1) / gridDim.x, int64_t(kMinUnits));
-    const int64_t u0 = int64_t(blockIdx.x) * quota;
-    if (u0 >= total) {
-        if (threadIdx.x == 0 && !a.by_segment) a.desc[blockIdx.x].pieces = 0;
-        return;
-    }
-    if (a.B <= kThreads) {
-        if (mine && incl - mine <= u0 && u0 < incl) {
-            sm.b = threadIdx.x;
-            sm.off = u0 - (incl - mine);
-        }
+    int b, ht, c0;              // sequence; head and tile; how much of their cost lies before this range
+    int64_t quota = 0, left;
+    Seq seq;
+    if (kDirect) {
+        b = int(blockIdx.x) / per_seq;
+        ht = int(blockIdx.x) % per_seq;
+        seq = seq_of(a, b);
+        c0 = 0;
+        left = seq.cost();
     } else {
-        int64_t before = 0;
+        int64_t total = 0, mine = 0, incl = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + threadIdx.x;
             mine = b < a.B ? int64_t(seq_of(a, b).cost()) * per_seq : 0;
             int64_t t;
-            incl = before + block_scan(mine, sm.sums, t);
+            incl = total + block_scan<kWarps>(mine, sm.sums, t);
+            total += t;
+        }
+        quota = max((total + gridDim.x - 1) / gridDim.x, int64_t(kMinUnits));
+        const int64_t u0 = int64_t(blockIdx.x) * quota;
+        if (u0 >= total) {
+            if (threadIdx.x == 0 && !a.by_segment) a.desc[blockIdx.x].pieces = 0;
+            return;
+        }
+        if (a.B <= kThreads) {
             if (mine && incl - mine <= u0 && u0 < incl) {
-                sm.b = b;
+                sm.b = threadIdx.x;
                 sm.off = u0 - (incl - mine);
             }
-            before += t;
-            if (before > u0) break;
+        } else {
+            int64_t before = 0;
+            for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+                const int b = b0 + threadIdx.x;
+                mine = b < a.B ? int64_t(seq_of(a, b).cost()) * per_seq : 0;
+                int64_t t;
+                incl = before + block_scan<kWarps>(mine, sm.sums, t);
+                if (mine && incl - mine <= u0 && u0 < incl) {
+                    sm.b = b;
+                    sm.off = u0 - (incl - mine);
+                }
+                before += t;
+                if (before > u0) break;
+            }
         }
+        __syncthreads();
+        b = sm.b;
+        seq = seq_of(a, b);
+        ht = int(sm.off / seq.cost());                         // head and tile
+        c0 = int(sm.off - int64_t(ht) * seq.cost());       // and how much of its cost lies before this range
+        left = min(quota, total - u0);
     }
-    __syncthreads();
-    int b = sm.b;
-    Seq seq = seq_of(a, b);
-    int ht = int(sm.off / seq.cost());                     // head and tile
-    int c0 = int(sm.off - int64_t(ht) * seq.cost());       // and how much of its cost lies before this range
-    int64_t left = min(quota, total - u0);
     Desc cut{0, 0, 0, 0, 0, 0};    // the segment that goes on behind this range, if it begins in it
     const bool odd_page = a.pool.per_page & 1;             // a pair may lie in two pages
     uint64_t* full = sm.full[warp];
@@ -537,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
                     wo[(8 * t + 2 * q + (c & 1)) * S::kPitch + 16 * i + g + 8 * (c >> 1)] = st.o[t][i][c];
         __syncthreads();
         const bool begins = v0 == 0, ends = c1 == seq.cost();
-        if (begins) {
+        if (!kDirect && begins) {
             // its other pieces are the next ranges' first ones
             const int pieces = ends ? 1 : 1 + int((seq.cost() - c1 + quota - 1) / quota);
             cut = Desc{b, h, ht % a.RT, pieces, int(blockIdx.x), rows};
@@ -557,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
                 l += f * sm.l[w][r];
                 o += f * reinterpret_cast<const float*>(sm.ring[w])[r * S::kPitch + d];
             }
-            if (begins && ends) {
+            if (kDirect || (begins && ends)) {
                 a.o[row_at(r0 + r) + d] = __float2half_rn(l == 0.f ? 0.f : o / l);
             } else {
                 part[r * (D + 2) + d] = o;
@@ -577,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_kernel(co
             seq = seq_of(a, ++b);
         }
     }
-    if (!a.by_segment && threadIdx.x == 0) a.desc[blockIdx.x] = cut;     // of the last segment begun: the only one that can go on
+    if (!kDirect && !a.by_segment && threadIdx.x == 0) a.desc[blockIdx.x] = cut;     // of the last segment begun: the only one that can go on
     if (!ok) {
         // a wait ran out: give the copies under way their time to land before the CTA ends
         for (int i = 0; i < kSlots; ++i) mbar_wait_for(&full[i], phase ^ (i < int(slot)), kWaitLimitCycles / 16);
@@ -660,21 +681,21 @@ size_t workspace_of(const tern_cache* c, int64_t T, int64_t heads) {
     return (desc + n * 2 * size_t(8 * nt * (c->head_dim + 2)) * 4 + 255) & ~size_t(255);
 }
 
-template <int D, int NT>
-tern_status launch(Args& a, void* workspace, cudaStream_t stream) {
-    using S = Smem<D, NT>;
+template <int D, int NT, bool kDirect>
+bool configure() {
     static std::mutex mu;
     static bool configured[64] = {false};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TERN_ERR_CUDA;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!configured[dev]) {
-            if (cudaFuncSetAttribute(attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(S))) != cudaSuccess)
-                return TERN_ERR_CUDA;
-            configured[dev] = true;
-        }
-    }
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!configured[dev])
+        configured[dev] = cudaFuncSetAttribute(attention_kernel<D, NT, kDirect>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(sizeof(Smem<D, NT, kDirect ? kDirectWarps : kSplitWarps>))) == cudaSuccess;
+    return configured[dev];
+}
+
+template <int D, int NT>
+tern_status launch(Args& a, void* workspace, cudaStream_t stream) {
     const int n = ctas_of(NT);
     a.RT = (a.T * a.G + 8 * NT - 1) / (8 * NT);
     a.desc = static_cast<Desc*>(workspace);
@@ -687,13 +708,25 @@ tern_status launch(Args& a, void* workspace, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(n), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(S);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attention_kernel<D, NT>, a) != cudaSuccess) return TERN_ERR_CUDA;
+    // The most units that a segment can have, by the table's width and the window: up to kDirectUnits of them a CTA of eight
+    // warps per segment is through sooner than the even split with its second kernel.
+    int64_t most = (a.pool.width * a.pool.per_page + 1) / 2;
+    if (a.window > 0) most = std::min(most, (int64_t(a.sinks) + kPair - 1) / kPair + (int64_t(a.window) + a.T + kPair - 2) / kPair + 1);
+    if (most <= kDirectUnits && segments <= 0x7fffffff) {
+        if (!configure<D, NT, true>()) return TERN_ERR_CUDA;
+        cfg.gridDim = dim3(unsigned(segments), 1, 1);
+        cfg.blockDim = dim3(kDirectWarps * 32, 1, 1);
+        cfg.dynamicSmemBytes = sizeof(Smem<D, NT, kDirectWarps>);
+        return cudaLaunchKernelEx(&cfg, attention_kernel<D, NT, true>, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
+    }
+    if (!configure<D, NT, false>()) return TERN_ERR_CUDA;
+    cfg.gridDim = dim3(unsigned(n), 1, 1);
+    cfg.blockDim = dim3(kSplitWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = sizeof(Smem<D, NT, kSplitWarps>);
+    if (cudaLaunchKernelEx(&cfg, attention_kernel<D, NT, false>, a) != cudaSuccess) return TERN_ERR_CUDA;
     cfg.gridDim = dim3(unsigned(a.ndesc), unsigned(a.T * a.G < 8 * NT ? a.T * a.G : 8 * NT), 1);
     cfg.blockDim = dim3(kJoin, 1, 1);
     cfg.dynamicSmemBytes = 0;
