@@ -333,8 +333,8 @@ tern_status tern_nib_dequant(const tern_nib_weight* w, tern_half* out, tern_stre
 size_t tern_nib_linear_workspace_bytes(const tern_nib_weight* w, int64_t M);
 
 /* y [M, N] = x [M, K] . W^T (x, y device, fp16, row-major), fp32 accumulation, one rounding to
- * fp16. Any M >= 0 (0 is a no-op). x and y must not overlap. Workspace rule, streams and capture
- * as for tern_linear.                                                                     */
+ * fp16. 0 <= M <= 2^22 (0 is a no-op). x and y must not overlap. Workspace rule, streams and capture
+ * as for tern_linear. An infinity in x makes its token's y infinite or NaN.               */
 tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half* x, int64_t M, tern_half* y, void* workspace,
                             size_t workspace_bytes, tern_stream stream);
 

@@ -502,6 +502,10 @@ class NibWeight:
             k = self.__dict__["_seen"] = (c, ctypes.byref(c), self.codes.get_device(), {})
         return k
 
+    def __getstate__(self):
+        # a copy has tensors, and so a descriptor, of its own
+        return {k: v for k, v in self.__dict__.items() if k != "_seen"}
+
     def c_struct(self) -> _lib.TernNibWeightC:
         return self._known()[0]
 
@@ -640,6 +644,9 @@ class PagedCache:
         self._c = _lib.TernCacheC(pool.data_ptr(), self.pages, self.page, self.kv_heads, self.head_dim)
         self._ref, self._dev = ctypes.byref(self._c), pool.get_device()
         self._ws = {}
+
+    def __reduce__(self):
+        return type(self), (self.pool,)
 
     @classmethod
     def empty(cls, pages: int, page: int, kv_heads: int, head_dim: int, device="cuda") -> "PagedCache":

@@ -45,6 +45,7 @@ constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kMaxStages = 4;
 constexpr int kStageBlocks = 32;           // blocks of 128 columns in a stage at most
 constexpr int64_t kMaxM = 16;
+constexpr int64_t kMostTokens = int64_t(1) << 22;    // of a call: 65535 tiles of the least rows many tokens get, 128, hold them
 constexpr int kTf32Per = 4;                // groups of a block from which the correction is a tf32 product
 
 struct Args {
@@ -415,7 +416,7 @@ extern "C" tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half
                                        void* workspace, size_t workspace_bytes, tern_stream stream) {
     const tern_status st = check_nib(w);
     if (st != TERN_OK) return st;
-    if (M < 0 || M > (int64_t(1) << 31)) return TERN_ERR_SHAPE;
+    if (M < 0 || M > kMostTokens) return TERN_ERR_SHAPE;
     if (M == 0) return TERN_OK;
     if (!x || !y) return TERN_ERR_NULL;
     if (!aligned16(x) || !aligned16(y)) return TERN_ERR_ALIGN;

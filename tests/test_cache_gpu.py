@@ -7,6 +7,8 @@ below fp16's normal range is off by up to 2^-25 (n tokens of the largest |v|, ov
 rounded (2^-11 |o|), and a score is off by at most D 2^-22 |q| |k| scale, which moves every probability by
 that share twice (its own and the sum's)."""
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -149,6 +151,30 @@ def test_attention_with_a_window_and_sinks(window, sinks, T):
     q = rng.standard_normal((4, T, 6, 128)).astype(np.float16)
     o = api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array(lens, np.int32)), window=window, sinks=sinks).cpu().numpy()
     check_attention(o, q, K, V, lens, [T] * 4, 128**-0.5, window, sinks)
+
+
+@pytest.mark.parametrize("window", [1000, 2**31 - 60, 2**31 - 1, 2**40])
+def test_queries_before_token_zero_and_windows_past_every_length(window):
+    """Sequences with fewer cached tokens than queries: the first queries see nothing, the others all there is."""
+    rng = np.random.default_rng(7)
+    lens, T = [5, 64, 40, 0, 200], 64
+    cache, table, K, V, _, _ = make(rng, lens, 32, 2, 64)
+    q = rng.standard_normal((5, T, 4, 64)).astype(np.float16)
+    o = api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array(lens, np.int32)), window=window).cpu().numpy()
+    check_attention(o, q, K, V, lens, [T] * 5, 64**-0.5, 0, 0)
+    assert not o[0, :59].any() and not o[3].any() and not o[2, :24].any()
+
+
+def test_a_copied_cache_is_a_cache_of_its_own():
+    rng = np.random.default_rng(8)
+    cache, table, K, V, k, v = make(rng, [50], 32, 2, 64)
+    q = cuda(rng.standard_normal((1, 1, 4, 64)).astype(np.float16))
+    where, lens = cuda(table), cuda(np.array([50], np.int32))
+    o = api.cache_attention(q, cache, where, lens)
+    twin = copy.deepcopy(cache)
+    assert twin.pool.data_ptr() != cache.pool.data_ptr()
+    cache.pool.zero_()
+    assert torch.equal(api.cache_attention(q, twin, where, lens), o)
 
 
 def test_attention_of_a_padded_batch_leaves_the_rest():

@@ -175,3 +175,10 @@ def test_oracle_fit_meets_the_formula_and_halves_the_step():
         step = s.astype(np.float64)[..., None]
         assert (err <= 0.5 * step + 16 * step * 2.0**-11 + np.abs(W).max() * 2.0**-11).all()
         assert c.min() >= 0 and c.max() <= 15 and len(np.unique(c)) == (16 if offset else 15)
+
+
+def test_the_most_tokens_of_a_call(lib):
+    w = ctypes.byref(nib(N=16, K=128))
+    call = lambda M: lib.tern_nib_linear(w, None, M, F, None, 0, None)  # noqa: E731
+    assert call(1 << 22) == S["TERN_ERR_NULL"]                   # of a size that is taken
+    assert call((1 << 22) + 1) == S["TERN_ERR_SHAPE"]

@@ -6,6 +6,8 @@ products, of which each addition is off by at most 2^-23 of the largest partial 
 16 tokens the weights are rounded to fp16 first, half a step of each, 2^-11 sum |w x|; one rounding of the
 result, 2^-11 |y| (2^-25 below fp16's normal range). The norm of all errors is held to two such roundings."""
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -219,6 +221,18 @@ def test_linear_repeats_to_the_bit_on_any_stream_and_in_a_graph(M):
         assert torch.equal(yg, first) and torch.equal(yy, first)
     assert all(torch.equal(o, first) for o in outs)
     del g
+
+
+def test_a_copied_weight_is_a_weight_of_its_own():
+    rng = np.random.default_rng(4)
+    w = weight(*draw(rng, 48, 256, 64, True))
+    x = torch.from_numpy(rng.standard_normal((2, 256), dtype=np.float32).astype(np.float16)).cuda()
+    y = api.nib_linear(x, w)
+    twin = copy.deepcopy(w)
+    assert twin.codes.data_ptr() != w.codes.data_ptr()
+    w.codes.zero_()
+    assert torch.equal(api.nib_linear(x, twin), y)
+    assert not torch.equal(api.nib_linear(x, w), y)
 
 
 def test_no_tokens():
