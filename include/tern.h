@@ -378,8 +378,10 @@ tern_status tern_cache_read(const tern_cache* cache, tern_half* k, tern_half* v,
                             const int32_t* table, int64_t width, const int32_t* start, const int32_t* counts,
                             tern_stream stream);
 
-/* Bytes of workspace tern_cache_attention needs (0 when the arguments are invalid).       */
-size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, int64_t T, int64_t heads);
+/* Bytes of workspace tern_cache_attention needs with these arguments: 0 where no sequence can be long, by the
+ * table's width and the window, and when the arguments are invalid.                       */
+size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, int64_t T, int64_t heads, int64_t width,
+                                            int64_t window, int64_t sinks);
 
 /* o [B, T, heads, head_dim] = softmax(scale q K^T + mask) V for the last tokens of each sequence over its
  * cache (q, o device, fp16): decoding (T = 1), drafted tokens, short chunks; T <= 64. heads is a

@@ -61,7 +61,7 @@ EXPORTS = {
                                      _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
     "tern_cache_read": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
                                    _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
-    "tern_cache_attention_workspace_bytes": (_c.c_size_t, [_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64]),
+    "tern_cache_attention_workspace_bytes": (_c.c_size_t, [_c.c_void_p] + [_c.c_int64] * 6),
     "tern_cache_attention": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p,
                                         _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_float, _c.c_int64, _c.c_int64,
                                         _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),

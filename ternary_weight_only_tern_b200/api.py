@@ -524,10 +524,10 @@ def _nib_check_shape(N: int, K: int, group: int):
 def _nib_empty(N: int, K: int, group: int, offset: bool, like: torch.Tensor) -> NibWeight:
     _nib_check_shape(N, K, group)
     strips = -(-N // 16)
+    scale = like.new_empty((strips, K // group, 16), dtype=_F16)
     w = NibWeight.__new__(NibWeight)       # of the right shapes by construction
-    w.__dict__.update(N=N, K=K, group=group, codes=like.new_empty((strips, K // GROUP, 256), dtype=_I32),
-                      scale=like.new_empty((strips, K // group, 16), dtype=_F16),
-                      mu=like.new_empty((strips, K // group, 16), dtype=_F16) if offset else None, static=False)
+    w.__dict__.update(N=N, K=K, group=group, codes=like.new_empty((strips, K // GROUP, 256), dtype=_I32), scale=scale,
+                      mu=torch.empty_like(scale) if offset else None, static=False)
     return w
 
 
@@ -662,12 +662,13 @@ class PagedCache:
     def nbytes(self) -> int:
         return self.pool.numel()
 
-    def workspace_bytes(self, B: int, T: int, heads: int) -> int:
+    def workspace_bytes(self, B: int, T: int, heads: int, width: int, window: int = 0, sinks: int = 0) -> int:
         """tern_cache_attention_workspace_bytes, remembered per size."""
-        n = self._ws.get((B, T, heads))
+        key = (B, T, heads, width, window, sinks)
+        n = self._ws.get(key)
         if n is None:
             with torch.cuda.device(self._dev):
-                n = self._ws[B, T, heads] = int(_lib.load().tern_cache_attention_workspace_bytes(self._ref, B, T, heads))
+                n = self._ws[key] = int(_lib.load().tern_cache_attention_workspace_bytes(self._ref, *key))
         return n
 
 
@@ -720,7 +721,8 @@ def cache_read(cache: PagedCache, table: torch.Tensor, start: torch.Tensor, T: i
     ta, width = _table(table, B, dev)
     shape = (B, T, cache.kv_heads, cache.head_dim)
     if out is None:
-        k, v = table.new_empty(shape, dtype=_F16), table.new_empty(shape, dtype=_F16)
+        k = table.new_empty(shape, dtype=_F16)
+        v = torch.empty_like(k)
     else:
         k, v = out
         for t, name in ((k, "out[0]"), (v, "out[1]")):
@@ -758,9 +760,9 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, len
         if out.shape != q.shape:
             raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
     ta, width = _table(table, B, dev)
-    need = cache._ws.get((B, T, heads))
+    need = cache._ws.get((B, T, heads, width, window, sinks))
     if need is None:
-        need = cache.workspace_bytes(B, T, heads)
+        need = cache.workspace_bytes(B, T, heads, width, window, sinks)
     ws = wsb = 0
     if need or workspace is not None:
         workspace, wsb = _scratch(workspace, need, q)

@@ -37,7 +37,9 @@ namespace {
 using namespace kv;
 
 constexpr int kSplitWarps = 4;             // warps of a CTA where segments are split
-constexpr int kDirectWarps = 8;            // and where each has a CTA of its own
+constexpr int kFewWarps = 8, kManyWarps = 16;   // and where each has a CTA of its own: many where every CTA has an SM to itself
+                                           // (16 sequences of 8 kv heads, 300 tokens 7.3 us against 8.4, 1000 tokens 10.3 against
+                                           // 13.4), few where not (64 sequences: 15.8 against 25.5, 26.2 against 35.6)
 constexpr int kDirectUnits = 36;           // units of a segment up to which it has (measured, 1 / 4 / 16 / 64 sequences of 8 kv heads:
                                            // 300 tokens 6.8 6.9 8.4 15.9 us against 9.0 10.1 12.2 19.2 split; 1000 tokens
                                            // 10.0 10.0 13.4 26.4 against 9.4 10.8 13.9 28.1; 2000 15.2 15.2 20.6 38.8
@@ -346,11 +348,14 @@ struct Smem {
     float m[kWarps][kRows], l[kWarps][kRows];
 };
 
-// kDirect: CTA i takes the whole of segment i, and nothing is split or joined.
-template <int D, int NT, bool kDirect>
-__global__ void __launch_bounds__((kDirect ? kDirectWarps : kSplitWarps) * 32, kDirect ? (NT == 1 ? 2 : 1) : (NT == 1 ? 4 : 3))
+// CTAs of an SM: what the registers of each variant allow.
+constexpr int resident(int nt, int direct) { return direct ? (nt == 1 && direct == kFewWarps ? 2 : 1) : (nt == 1 ? 4 : 3); }
+
+// kDirect > 0: CTA i, of so many warps, takes the whole of segment i, and nothing is split or joined.
+template <int D, int NT, int kDirect>
+__global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, resident(NT, kDirect))
     attention_kernel(const Args a) {
-    constexpr int kWarps = kDirect ? kDirectWarps : kSplitWarps, kThreads = kWarps * 32;
+    constexpr int kWarps = kDirect ? kDirect : kSplitWarps, kThreads = kWarps * 32;
     using S = Smem<D, NT, kWarps>;
     constexpr int W = D / 32, NG = D / kGrp, kRows = 8 * NT, U = unit_bytes(D);   // U: bytes of a block
     extern __shared__ __align__(128) uint8_t raw[];
@@ -675,7 +680,18 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
 
 // Rows per tile: 8, or 16 where a kv head has more (the cache is then read half as often).
 int tiles_of(int64_t T, int64_t G) { return T * G > 8 ? 2 : 1; }
-int ctas_of(int nt) { return sm_count() * (nt == 1 ? 4 : 3); }
+int ctas_of(int nt) { return sm_count() * resident(nt, 0); }
+
+// Whether no segment can be long: the most units that one can have, by the table's width and the window. Up to kDirectUnits
+// of them a CTA per segment is through sooner than the even split with its second kernel.
+bool direct_of(int64_t width, int per_page, int window, int sinks, int64_t T, int64_t segments) {
+    int64_t most = (width * per_page + 1) / 2;
+    if (window > 0) most = std::min(most, (int64_t(sinks) + kPair - 1) / kPair + (window + T + kPair - 2) / kPair + 1);
+    return most <= kDirectUnits && segments <= 0x7fffffff;
+}
+
+int64_t row_tiles(int64_t T, int64_t G) { return (T * G + 8 * tiles_of(T, G) - 1) / (8 * tiles_of(T, G)); }
+int at_most_int(int64_t v) { return int(std::min<int64_t>(v, 0x7fffffff)); }
 
 size_t workspace_of(const tern_cache* c, int64_t T, int64_t heads) {
     const int nt = tiles_of(T, heads / c->kv_heads);
@@ -684,7 +700,7 @@ size_t workspace_of(const tern_cache* c, int64_t T, int64_t heads) {
     return (desc + n * 2 * size_t(8 * nt * (c->head_dim + 2)) * 4 + 255) & ~size_t(255);
 }
 
-template <int D, int NT, bool kDirect>
+template <int D, int NT, int kDirect>
 bool configure() {
     static std::mutex mu;
     static bool configured[64] = {false};
@@ -693,14 +709,23 @@ bool configure() {
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev])
         configured[dev] = cudaFuncSetAttribute(attention_kernel<D, NT, kDirect>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(sizeof(Smem<D, NT, kDirect ? kDirectWarps : kSplitWarps>))) == cudaSuccess;
+                                               int(sizeof(Smem<D, NT, kDirect ? kDirect : kSplitWarps>))) == cudaSuccess;
     return configured[dev];
+}
+
+template <int D, int NT, int kWarps>
+tern_status launch_direct(cudaLaunchConfig_t& cfg, const Args& a, int64_t segments) {
+    if (!configure<D, NT, kWarps>()) return TERN_ERR_CUDA;
+    cfg.gridDim = dim3(unsigned(segments), 1, 1);
+    cfg.blockDim = dim3(kWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = sizeof(Smem<D, NT, kWarps>);
+    return cudaLaunchKernelEx(&cfg, attention_kernel<D, NT, kWarps>, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
 template <int D, int NT>
 tern_status launch(Args& a, void* workspace, cudaStream_t stream) {
     const int n = ctas_of(NT);
-    a.RT = (a.T * a.G + 8 * NT - 1) / (8 * NT);
+    a.RT = int(row_tiles(a.T, a.G));
     a.desc = static_cast<Desc*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ((size_t(n) * sizeof(Desc) + 255) & ~size_t(255)));
     a.status = async_status_word();
@@ -714,32 +739,27 @@ tern_status launch(Args& a, void* workspace, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // The most units that a segment can have, by the table's width and the window: up to kDirectUnits of them a CTA of eight
-    // warps per segment is through sooner than the even split with its second kernel.
-    int64_t most = (a.pool.width * a.pool.per_page + 1) / 2;
-    if (a.window > 0) most = std::min(most, (int64_t(a.sinks) + kPair - 1) / kPair + (int64_t(a.window) + a.T + kPair - 2) / kPair + 1);
-    if (most <= kDirectUnits && segments <= 0x7fffffff) {
-        if (!configure<D, NT, true>()) return TERN_ERR_CUDA;
-        cfg.gridDim = dim3(unsigned(segments), 1, 1);
-        cfg.blockDim = dim3(kDirectWarps * 32, 1, 1);
-        cfg.dynamicSmemBytes = sizeof(Smem<D, NT, kDirectWarps>);
-        return cudaLaunchKernelEx(&cfg, attention_kernel<D, NT, true>, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
+    if (direct_of(a.pool.width, a.pool.per_page, a.window, a.sinks, a.T, segments)) {
+        if constexpr (NT == 1)      // (16 rows need the registers of 8 warps)
+            if (segments <= sm_count()) return launch_direct<D, NT, kManyWarps>(cfg, a, segments);
+        return launch_direct<D, NT, kFewWarps>(cfg, a, segments);
     }
-    if (!configure<D, NT, false>()) return TERN_ERR_CUDA;
+    if (!configure<D, NT, 0>()) return TERN_ERR_CUDA;
     cfg.gridDim = dim3(unsigned(n), 1, 1);
     cfg.blockDim = dim3(kSplitWarps * 32, 1, 1);
     cfg.dynamicSmemBytes = sizeof(Smem<D, NT, kSplitWarps>);
-    if (cudaLaunchKernelEx(&cfg, attention_kernel<D, NT, false>, a) != cudaSuccess) return TERN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, attention_kernel<D, NT, 0>, a) != cudaSuccess) return TERN_ERR_CUDA;
     cfg.gridDim = dim3(unsigned(a.ndesc), unsigned(a.T * a.G < 8 * NT ? a.T * a.G : 8 * NT), 1);
     cfg.blockDim = dim3(kJoin, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, a) == cudaSuccess ? TERN_OK : TERN_ERR_CUDA;
 }
 
-tern_status check_attention(const tern_cache* c, int64_t B, int64_t T, int64_t heads) {
+tern_status check_attention(const tern_cache* c, int64_t B, int64_t T, int64_t heads, int64_t width, int64_t window, int64_t sinks) {
     const tern_status st = check_cache(c);
     if (st != TERN_OK) return st;
-    if (!batch_ok(B, T, 0) || T > 64 || heads <= 0 || heads % c->kv_heads || heads > 65535) return TERN_ERR_SHAPE;
+    if (!batch_ok(B, T, width) || T > 64 || heads <= 0 || heads % c->kv_heads || heads > 65535 || window < 0 || sinks < 0)
+        return TERN_ERR_SHAPE;
     return TERN_OK;
 }
 
@@ -749,8 +769,11 @@ tern_status check_attention(const tern_cache* c, int64_t B, int64_t T, int64_t h
 using namespace tern;
 using namespace tern::kv;
 
-extern "C" size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, int64_t T, int64_t heads) {
-    if (check_attention(cache, B, T, heads) != TERN_OK || B == 0 || T == 0) return 0;
+extern "C" size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, int64_t T, int64_t heads,
+                                                       int64_t width, int64_t window, int64_t sinks) {
+    if (check_attention(cache, B, T, heads, width, window, sinks) != TERN_OK || B == 0 || T == 0) return 0;
+    const int64_t segments = B * cache->kv_heads * row_tiles(T, heads / cache->kv_heads);
+    if (direct_of(width, cache->page / kTok, at_most_int(window), at_most_int(sinks), T, segments)) return 0;
     return workspace_of(cache, T, heads);
 }
 
@@ -758,15 +781,15 @@ extern "C" tern_status tern_cache_attention(const tern_cache* cache, const tern_
                                             int64_t heads, const int32_t* table, int64_t width, const int32_t* lens,
                                             const int32_t* counts, float scale, int64_t window, int64_t sinks,
                                             tern_half* o, void* workspace, size_t workspace_bytes, tern_stream stream) {
-    const tern_status st = check_attention(cache, B, T, heads);
+    const tern_status st = check_attention(cache, B, T, heads, width, window, sinks);
     if (st != TERN_OK) return st;
-    if (!batch_ok(B, T, width) || window < 0 || sinks < 0 || !(fabsf(scale) <= kMaxScale)) return TERN_ERR_SHAPE;
+    if (!(fabsf(scale) <= kMaxScale)) return TERN_ERR_SHAPE;
     if (B == 0 || T == 0) return TERN_OK;
     if (!q || !o || !lens || (!table && width)) return TERN_ERR_NULL;
     if (!aligned16(q) || !aligned16(o)) return TERN_ERR_ALIGN;
     const size_t bytes = size_t(B) * size_t(T) * size_t(heads) * size_t(cache->head_dim) * 2;
     if (overlaps(q, bytes, o, bytes)) return TERN_ERR_SHAPE;
-    const size_t need = tern_cache_attention_workspace_bytes(cache, B, T, heads);
+    const size_t need = tern_cache_attention_workspace_bytes(cache, B, T, heads, width, window, sinks);
     if (need && (!workspace || workspace_bytes < need)) return TERN_ERR_WORKSPACE;
     if (workspace && !aligned16(workspace)) return TERN_ERR_ALIGN;
     Args a{};
@@ -775,8 +798,8 @@ extern "C" tern_status tern_cache_attention(const tern_cache* cache, const tern_
     a.o = reinterpret_cast<__half*>(o);
     a.lens = lens;
     a.counts = counts;
-    a.window = int(window < 0x7fffffff ? window : 0x7fffffff);
-    a.sinks = int(sinks < 0x7fffffff ? sinks : 0x7fffffff);
+    a.window = at_most_int(window);
+    a.sinks = at_most_int(sinks);
     a.B = int(B);
     a.T = int(T);
     a.heads = int(heads);

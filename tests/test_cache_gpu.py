@@ -333,7 +333,7 @@ def test_streams_graphs_and_repeats_agree_to_the_bit():
             outs += [api.cache_attention(q, cache, tab, n) for _ in range(3)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, first) for o in outs)
-    ws = torch.full((max(1, cache.workspace_bytes(4, 1, 16)),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(1, cache.workspace_bytes(4, 1, 16, table.shape[1])),), 0xFF, dtype=torch.uint8, device="cuda")
     qg, lg = torch.zeros_like(q), torch.ones_like(n)
     graphs = []
     for _ in range(2):                                   # two graphs, one workspace, one after the other

@@ -96,7 +96,7 @@ def test_a_bad_cache_is_refused_everywhere(lib, kw, err):
     assert lib.tern_cache_read(c, F, F, 1, 1, F, 4, F, None, None) == e
     heads = kw.get("heads", 2) or 2
     assert lib.tern_cache_attention(c, F, 1, 1, heads, F, 4, F, None, 1.0, 0, 0, F * 2, None, 0, None) == e
-    assert lib.tern_cache_attention_workspace_bytes(c, 1, 1, heads) == 0
+    assert lib.tern_cache_attention_workspace_bytes(c, 1, 1, heads, 1 << 20, 0, 0) == 0
 
 
 @pytest.mark.parametrize("name", ["tern_cache_append", "tern_cache_read"])
@@ -117,7 +117,7 @@ def test_append_and_read_refusals(lib, name):
 
 def test_attention_refusals(lib):
     c = kv()
-    call = lambda q=F, B=2, T=3, H=8, table=F, width=4, lens=F, scale=0.1, window=0, sinks=0, o=F * 2, ws=F * 4, wsb=1 << 40: \
+    call = lambda q=F, B=2, T=3, H=8, table=F, width=400, lens=F, scale=0.1, window=0, sinks=0, o=F * 2, ws=F * 4, wsb=1 << 40: \
         lib.tern_cache_attention(ctypes.byref(c), q, B, T, H, table, width, lens, None, scale, window, sinks, o, ws, wsb, None)  # noqa: E731
     assert call(B=0, q=None) == S["TERN_OK"]
     assert call(T=0, o=None) == S["TERN_OK"]
@@ -128,7 +128,12 @@ def test_attention_refusals(lib):
         assert call(**kw) == S["TERN_ERR_NULL"], kw
     for kw in (dict(q=F + 2), dict(o=F * 2 + 8), dict(ws=F * 4 + 4)):
         assert call(**kw) == S["TERN_ERR_ALIGN"], kw
-    need = lib.tern_cache_attention_workspace_bytes(ctypes.byref(c), 2, 3, 8)
+    size = lambda width, window=0, sinks=0: lib.tern_cache_attention_workspace_bytes(  # noqa: E731
+        ctypes.byref(c), 2, 3, 8, width, window, sinks)
+    need = size(400)
+    assert size(400, -1) == size(400, 0, -1) == size(-1) == 0
+    assert size(4) == size(400, 100) == size(400, 1, 5) == 0           # no sequence can be long
+    assert size(400, 2**63 - 1, 2**63 - 1) == size(400, 100, 10**6) == need
     if need:
         assert call(ws=None) == S["TERN_ERR_WORKSPACE"]
         assert call(wsb=need - 1) == S["TERN_ERR_WORKSPACE"]
