@@ -22,8 +22,8 @@
 // shared memory. A (sequence, head, tile) that lies in one range is finished there; the pieces of one that
 // crosses ranges go to the workspace and a second, small kernel joins them, in the order of the ranges. Where no (sequence,
 // head, tile) can be long, by the table's width and the window, each has a CTA of its own instead.
-// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 85 us (3.9 TB/s), bound
-// by instruction issue (57 % of the slots, 337 warp instructions per block).
+// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 78.7 us (4.2 TB/s), bound
+// by instruction issue (61 % of the slots, 337 warp instructions per block) and what each segment's start and join cost.
 #include <math.h>
 
 #include <algorithm>
@@ -45,10 +45,11 @@ constexpr int kDirectUnits = 36;           // units of a segment up to which it 
                                            // 10.0 10.0 13.4 26.4 against 9.4 10.8 13.9 28.1; 2000 15.2 15.2 20.6 38.8
                                            // against 9.7 12.5 16.3 37.2)
 constexpr int kPair = 2 * kTok;            // tokens of a unit of work: two blocks
-constexpr int kSlots = 2;                  // units in a warp's ring
-constexpr int kSetup = 12;                 // what a (sequence, head, tile) costs beyond its units, in units (measured: its
-                                           // queries, pages and join; 64 sequences of up to 8192 tokens 112.7 us with 0,
-                                           // 102.8 with 4, 90.5 with 8, 86.1 with 12, 87.9 with 24)
+constexpr int kSlots = 3;                  // units in a warp's ring
+// What a (sequence, head, tile) costs beyond its units, in units: its queries, pages, first copies and join. Measured, 8 rows: 64
+// sequences of up to 8192 tokens 85.2 us with 8, 80.3 with 12, 78.7 with 16; 16 rows: 4 tokens of 32 sequences of up to 4000
+// 59.9 with 12, 57.4 with 16, 50.1 with 24, 51.6 with 32.
+constexpr int setup_of(int nt) { return nt == 1 ? 16 : 24; }
 constexpr int kMinUnits = 8;               // cost per CTA at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxScale = 1e4f;          // keeps scale q k of finite inputs finite
@@ -65,6 +66,7 @@ struct Args {
     const int32_t* lens;
     const int32_t* counts;
     int window, sinks;
+    int setup;                  // cost of a segment beyond its units
     int B, T, heads, G, RT;     // G = heads per kv head, RT = row tiles
     float scale;                // of the exponents (to base 2), > 0
     float slack;                // 8 / scale
@@ -72,12 +74,12 @@ struct Args {
     Desc* desc;                 // [ndesc]: by (sequence, head, tile) where these are fewer than the CTAs, else by CTA
     int ndesc;
     bool by_segment;
-    float* part;                // [gridDim.x][2 (continued from the range before, or not)][rows][D + 2]
+    float* part;                // [gridDim.x][2 (continued from the range before, or not)][rows][D + 4]: O, maximum, sum
     unsigned int* status;
 };
 
 template <int D, int NT>
-constexpr int part_floats() { return 8 * NT * (D + 2); }
+constexpr int part_floats() { return 8 * NT * (D + 4); }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     uint32_t d;
@@ -105,12 +107,14 @@ struct Seq {
     int cnt, first, last;       // queries; the tokens of the first and the last
     int blocks;                 // blocks 0 .. blocks - 1 may be read
     int sb, wb, n;              // pairs 0 .. sb - 1, then wb ..; n in all
+    int setup;
     __device__ __forceinline__ int pair(int v) const { return v < sb ? v : wb + v - sb; }
-    __device__ __forceinline__ int cost() const { return max(n, 1) + kSetup; }   // one unit at least, so that its rows are written
+    __device__ __forceinline__ int cost() const { return max(n, 1) + setup; }   // one unit at least, so that its rows are written
 };
 
 __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
     Seq s;
+    s.setup = a.setup;
     const int len = max(0, __ldg(a.lens + b));
     s.cnt = a.counts ? min(max(__ldg(a.counts + b), 0), a.T) : a.T;
     s.first = len - s.cnt;
@@ -143,15 +147,13 @@ struct State {
     float o[NT][D / 16][4];
 };
 
-// One block of 16 tokens in shared memory, j0 the first token. kMask: some row does not see some token. The maximum
-// is that of q k.
+// Scores q k of a block of 16 tokens in shared memory, j0 the first token: s [8 rows][token g: rows 2q, 2q + 1; token g + 8: the
+// same]. kMask: some row does not see some token; keep: masks of V's scales (tokens 2q, 2q + 1; 2q + 8, 2q + 9).
 template <int D, int NT, bool kMask>
-__device__ __forceinline__ void block_step(const uint8_t* u, int j0, const uint32_t (&qf)[NT][D / 32][4],
-                                           const float (&qx)[NT][2], const int (&pos)[NT][2], const Args& a,
-                                           State<D, NT>& st) {
+__device__ __forceinline__ void scores(const uint8_t* u, int j0, const uint32_t (&qf)[NT][D / 32][4], const float (&qx)[NT][2],
+                                       const int (&pos)[NT][2], const Args& a, float (&s)[NT][4], uint32_t (&keep)[2]) {
     constexpr int W = D / 32, NG = D / kGrp;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    float s[NT][4];                      // [8 rows][token g: rows 2q, 2q+1; token g + 8: the same]
     {
         uint32_t ka[W], kb[W];
         load_words(u + lane * W * 4, ka);
@@ -190,7 +192,6 @@ __device__ __forceinline__ void block_step(const uint8_t* u, int j0, const uint3
                 for (int i = 0; i < 4; ++i) s[t][i] += (i < 2 ? s0 : s1) * acc[t][i];
         }
     }
-    uint32_t keep[2];                    // masks of V's scales: tokens 2q, 2q + 1; 2q + 8, 2q + 9
     if (kMask) {
         // A V token that no row sees, or whose scales are not finite, counts as zeros in the product; a
         // row that sees one of the latter becomes NaN through its sum instead.
@@ -219,31 +220,49 @@ __device__ __forceinline__ void block_step(const uint8_t* u, int j0, const uint3
             keep[h] = ((kept >> (8 * q)) & 0xFu ? 0x0000FFFFu : 0u) | ((kept >> (8 * q + 4)) & 0xFu ? 0xFFFF0000u : 0u);
         }
     }
-    // The running maximum of a row moves only when some token is 2^8 above it (a probability may then be up to 2^8,
-    // well inside fp16): seldom, so the reduction over the 8 lanes of a column is not paid per block.
+}
+
+// The running maximum of a row moves only when some token is 2^8 above it (a probability may then be up to 2^8,
+// well inside fp16): seldom, so the reduction over the 8 lanes of a column is not paid per block.
+template <int D, int NT, int kBlocks>
+__device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Args& a, State<D, NT>& st) {
     bool up = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) up |= fmaxf(s[t][c], s[t][2 + c]) > st.m[t][c] + a.slack;
-    if (__any_sync(0xffffffffu, up)) {
+        for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(s[0][t][c], s[0][t][2 + c]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int k = 1; k < kBlocks; ++k) top = fmaxf(top, fmaxf(s[k][t][c], s[k][t][2 + c]));
+            up |= top > st.m[t][c] + a.slack;
+        }
+    if (!__any_sync(0xffffffffu, up)) return;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float m = fmaxf(fmaxf(s[t][c], s[t][2 + c]), st.m[t][c]);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const float f = m > st.m[t][c] ? ex2((st.m[t][c] - m) * a.scale) : 1.f;
-                st.m[t][c] = m;
-                st.l[t][c] *= f;
+        for (int c = 0; c < 2; ++c) {
+            float m = st.m[t][c];
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    st.o[t][i][c] *= f;
-                    st.o[t][i][2 + c] *= f;
-                }
+            for (int k = 0; k < kBlocks; ++k) m = fmaxf(m, fmaxf(s[k][t][c], s[k][t][2 + c]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float f = m > st.m[t][c] ? ex2((st.m[t][c] - m) * a.scale) : 1.f;
+            st.m[t][c] = m;
+            st.l[t][c] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                st.o[t][i][c] *= f;
+                st.o[t][i][2 + c] *= f;
             }
-    }
+        }
+}
+
+// A block's probabilities, and its V into O^T.
+template <int D, int NT, bool kMask>
+__device__ __forceinline__ void add_values(const uint8_t* u, const float (&s)[NT][4], const uint32_t (&keep)[2], const Args& a,
+                                           State<D, NT>& st) {
+    constexpr int W = D / 32, NG = D / kGrp;
+    const int lane = threadIdx.x & 31, q = lane & 3;
     uint32_t b0[NT], b1[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -337,7 +356,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
 template <int D, int NT, int kWarps>
 struct Smem {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kPitch = D + 1;
+    static constexpr int kPitch = D + 4;                               // 16-byte rows; a fragment's stores hit all banks once
     static constexpr int ring_bytes = kSlots * 2 * unit_bytes(D);      // of a warp; its O^T after the last unit
     static_assert(kRows * kPitch * 4 <= ring_bytes, "a warp's rows fit its ring");
     alignas(128) uint8_t ring[kWarps][ring_bytes];
@@ -345,15 +364,17 @@ struct Smem {
     int64_t sums[kWarps];
     int64_t off;
     int b;
-    float m[kWarps][kRows], l[kWarps][kRows];
+    float m[kWarps][kRows], l[kWarps][kRows], top[kRows];
 };
 
-// CTAs of an SM: what the registers of each variant allow.
-constexpr int resident(int nt, int direct) { return direct ? (nt == 1 && direct == kFewWarps ? 2 : 1) : (nt == 1 ? 4 : 3); }
+// CTAs of an SM: what leaves each variant its registers without spills. (D = 128, 8 rows: four CTAs of 128 registers took as long
+// over long sequences and longer over short ones, 4 sequences of up to 4000 tokens 13.3 us against 12.0; 16 rows: three took
+// 65.5 us over 131072 tokens against 61.1.)
+constexpr int resident(int D, int nt, int direct) { return direct ? (nt == 1 && direct == kFewWarps ? 2 : 1) : (nt == 1 ? 4 : 3) - (D == 128); }
 
 // kDirect > 0: CTA i, of so many warps, takes the whole of segment i, and nothing is split or joined.
 template <int D, int NT, int kDirect>
-__global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, resident(NT, kDirect))
+__global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, resident(D, NT, kDirect))
     attention_kernel(const Args a) {
     constexpr int kWarps = kDirect ? kDirect : kSplitWarps, kThreads = kWarps * 32;
     using S = Smem<D, NT, kWarps>;
@@ -432,7 +453,7 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
     while (left > 0) {
         const int h = ht / a.RT, r0 = (ht % a.RT) * kRows;
         const int c1 = int(min(int64_t(seq.cost()), c0 + left));
-        const int v0 = max(0, c0 - kSetup), v1 = max(0, c1 - kSetup);   // units of this range
+        const int v0 = max(0, c0 - a.setup), v1 = max(0, c1 - a.setup);   // units of this range
         if (v1 > 0) {
         const int rows = seq.cnt * a.G;                    // of this sequence and head; the tile's are r0 ..
         const bool live = r0 < rows && seq.n > 0;
@@ -528,13 +549,24 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
             const bool whole = have == 3u && ((v >= whole0 && v < whole1) || v < sink1);
             const uint8_t* unit = ring + slot * 2 * U;
             if (whole) {
+                float s[2][NT][4];
+                uint32_t none[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) block_step<D, NT, false>(unit + k * U, 0, qf, qx, pos, a, st);
+                for (int k = 0; k < 2; ++k) scores<D, NT, false>(unit + k * U, 0, qf, qx, pos, a, s[k], none);
+                raise<D, NT, 2>(s, a, st);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) add_values<D, NT, false>(unit + k * U, s[k], none, a, st);
             } else {
                 const int j0 = seq.pair(v) * kPair;
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k)
-                    if (have >> k & 1u) block_step<D, NT, true>(unit + k * U, j0 + k * kTok, qf, qx, pos, a, st);
+                    if (have >> k & 1u) {
+                        float s[1][NT][4];
+                        uint32_t keep[2];
+                        scores<D, NT, true>(unit + k * U, j0 + k * kTok, qf, qx, pos, a, s[0], keep);
+                        raise<D, NT, 1>(s, a, st);
+                        add_values<D, NT, true>(unit + k * U, s[0], keep, a, st);
+                    }
             }
             __syncwarp();       // every lane has read the slot: the unit kSlots further on goes there
             if (issued < n && ok) issue(issued++, slot);
@@ -556,6 +588,21 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
                     sm.l[warp][8 * t + 2 * q + c] = l;
                 }
             }
+        __syncthreads();
+        if (threadIdx.x < kRows) {      // each warp's factor of a row, in place of its maximum; the row's sum
+            const int r = threadIdx.x;
+            float top = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.m[w][r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = top == -INFINITY ? 1.f : ex2((sm.m[w][r] - top) * a.scale);
+                l += f * sm.l[w][r];
+                sm.m[w][r] = f;
+            }
+            sm.top[r] = top * a.scale;
+            sm.l[0][r] = l;
+        }
         float* wo = reinterpret_cast<float*>(ring);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -573,27 +620,24 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
             if (a.by_segment && threadIdx.x == 0) a.desc[b * per_seq + ht] = cut;
         }
         float* part = a.part + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * part_floats<D, NT>();
-        for (int i = threadIdx.x; i < kRows * D; i += kThreads) {
-            const int r = i / D, d = i % D;
+        for (int i = threadIdx.x; i < kRows * D / 4; i += kThreads) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
             if (r0 + r >= rows) break;
-            float m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][r]);
-            float l = 0.f, o = 0.f;
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = m == -INFINITY ? 1.f : exp2f((sm.m[w][r] - m) * a.scale);
-                l += f * sm.l[w][r];
-                o += f * reinterpret_cast<const float*>(sm.ring[w])[r * S::kPitch + d];
+                const float f = sm.m[w][r];
+                const float4 v = *reinterpret_cast<const float4*>(sm.ring[w] + (r * S::kPitch + d) * 4);
+                o[0] += f * v.x, o[1] += f * v.y, o[2] += f * v.z, o[3] += f * v.w;
             }
+            const float l = sm.l[0][r];
             if (kDirect || (begins && ends)) {
-                a.o[row_at(r0 + r) + d] = __float2half_rn(l == 0.f ? 0.f : o / l);
+                if (l == 0.f) o[0] = o[1] = o[2] = o[3] = 0.f;
+                const float by = l == 0.f ? 1.f : l;
+                *reinterpret_cast<uint2*>(a.o + row_at(r0 + r) + d) = make_uint2(pack_h2(o[0] / by, o[1] / by), pack_h2(o[2] / by, o[3] / by));
             } else {
-                part[r * (D + 2) + d] = o;
-                if (d == 0) {
-                    part[r * (D + 2) + D] = m * a.scale;
-                    part[r * (D + 2) + D + 1] = l;
-                }
+                *reinterpret_cast<float4*>(part + r * (D + 4) + d) = make_float4(o[0], o[1], o[2], o[3]);
+                if (d == 0) *reinterpret_cast<float2*>(part + r * (D + 4) + D) = make_float2(sm.top[r], l);
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings' next copies follow these accesses
@@ -620,7 +664,7 @@ constexpr int kJoin = 512;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
-    constexpr int kRows = 8 * NT, stride = D + 2, kPar = kJoin / D, kBatch = 4;
+    constexpr int kRows = 8 * NT, stride = D + 4, kPar = kJoin / D, kBatch = 4;
     __shared__ float sm_m[kPar], sm_l[kPar], sm_o[kPar][D];
     grid_launch_dependents();
     grid_dependency_wait();
@@ -680,7 +724,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
 
 // Rows per tile: 8, or 16 where a kv head has more (the cache is then read half as often).
 int tiles_of(int64_t T, int64_t G) { return T * G > 8 ? 2 : 1; }
-int ctas_of(int nt) { return sm_count() * resident(nt, 0); }
+int ctas_of(int D, int nt) { return sm_count() * resident(D, nt, 0); }
 
 // Whether no segment can be long: the most units that one can have, by the table's width and the window. Up to kDirectUnits
 // of them a CTA per segment is through sooner than the even split with its second kernel.
@@ -695,9 +739,9 @@ int at_most_int(int64_t v) { return int(std::min<int64_t>(v, 0x7fffffff)); }
 
 size_t workspace_of(const tern_cache* c, int64_t T, int64_t heads) {
     const int nt = tiles_of(T, heads / c->kv_heads);
-    const size_t n = size_t(ctas_of(nt));
+    const size_t n = size_t(ctas_of(c->head_dim, nt));
     const size_t desc = (n * sizeof(Desc) + 255) & ~size_t(255);
-    return (desc + n * 2 * size_t(8 * nt * (c->head_dim + 2)) * 4 + 255) & ~size_t(255);
+    return (desc + n * 2 * size_t(8 * nt * (c->head_dim + 4)) * 4 + 255) & ~size_t(255);
 }
 
 template <int D, int NT, int kDirect>
@@ -724,8 +768,9 @@ tern_status launch_direct(cudaLaunchConfig_t& cfg, const Args& a, int64_t segmen
 
 template <int D, int NT>
 tern_status launch(Args& a, void* workspace, cudaStream_t stream) {
-    const int n = ctas_of(NT);
+    const int n = ctas_of(D, NT);
     a.RT = int(row_tiles(a.T, a.G));
+    a.setup = setup_of(NT);
     a.desc = static_cast<Desc*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ((size_t(n) * sizeof(Desc) + 255) & ~size_t(255)));
     a.status = async_status_word();
