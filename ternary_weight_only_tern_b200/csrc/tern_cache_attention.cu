@@ -22,8 +22,8 @@
 // shared memory. A (sequence, head, tile) that lies in one range is finished there; the pieces of one that
 // crosses ranges go to the workspace and a second, small kernel joins them, in the order of the ranges. Where no (sequence,
 // head, tile) can be long, by the table's width and the window, each has a CTA of its own instead.
-// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 78.7 us (4.2 TB/s), bound
-// by instruction issue (61 % of the slots, 337 warp instructions per block) and what each segment's start and join cost.
+// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 79 us (4.2 TB/s), bound
+// by instruction issue (57 % of the slots, 300 warp instructions per block) and what each segment's start and join cost.
 #include <math.h>
 
 #include <algorithm>
