@@ -303,7 +303,7 @@ tern_status tern_rotate(const tern_half* x, int64_t M, int64_t K, const tern_hal
  *   scale, mu  fp16 [ceil(N / 16), K / group, 16], row r of the strip at 2 (r % 8) + r / 8.
  * Every pointer is device memory, caller-owned, 16-byte aligned.                          */
 typedef struct {
-    int64_t N, K;                /* K % 128 == 0                                         */
+    int64_t N, K;                /* K % 128 == 0; N <= 2^22, K <= 2^20                    */
     int32_t group;               /* 32, 64 or 128                                        */
     uint32_t flags;              /* 0 or TERN_WEIGHT_STATIC, as tern_weight.flags         */
     const uint32_t* codes;
@@ -354,7 +354,8 @@ tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half* x, int64_
  * Sequence b's token t lies in page table[b, t / page] (table int32 [B, width], device), at t % page. An
  * entry outside 0 .. pages - 1, or a t past the table's width, is no page: nothing is written there,
  * it reads as zeros, and attention does not see it. Pages may be shared by sequences that only
- * read them; two tokens of one tern_cache_append in the same place leave either.            */
+ * read them; two tokens of one tern_cache_append in the same place leave either. In the calls below B and
+ * heads are at most 65535, T (but for attention) and width at most 2^24.                  */
 typedef struct {
     uint8_t* pool;               /* [pages, kv_heads, page / 16, 18 head_dim], device, 16-byte aligned */
     int64_t pages;               /* pages kv_heads page / 16 < 2^31                       */

@@ -314,10 +314,14 @@ struct Plan {
 
 // Cycles of a call on the SMs: waves of CTAs, each 64 columns of K as long as measured for the slower of its MMAs and its
 // decoding (M = 2048, 12288 x 4096: 1400 with 256 rows and tokens, 815 with 128 rows; 64 tokens: 415, decoding), about 3000 for
-// a CTA's start and end; slices of K add a kernel and their sums' way through memory.
+// a CTA's start and end; slices of K add a kernel (8000: half of that leads 400 tokens at group 32, 4096 x 4096, to slices that
+// take 29.2 us against 22.1) and their sums' way through memory. At group 32 the decoding has four times
+// group 128's scales to load and choose (512 tokens, 9728 x 2560: 34.8 us with 600 for it, 43.4 with 400, by the tiles it leads
+// to; 1024 tokens, 12288 x 4096: 96.9 against 120).
 Plan plan_of(const tern_nib_weight& w, int64_t M) {
     const int KB = int(w.K / kGroup);
     const int64_t sms = sm_count();
+    const double decode = w.group == 32 ? 600.0 : 400.0;      // of 128 rows and 64 columns
     Plan best{};
     double least = 1e30;
     for (int h = 1; h <= 2; ++h)
@@ -328,8 +332,8 @@ Plan plan_of(const tern_nib_weight& w, int64_t M) {
                 const int slice = (KB + slices - 1) / slices, real = (KB + slice - 1) / slice;
                 const int64_t rows = (w.N + kRowsM * h - 1) / (kRowsM * h), toks = (M + bt - 1) / bt;
                 const int64_t waves = (rows * toks * real + sms - 1) / sms;
-                double c = double(waves) * (2.0 * slice * (h == 1 ? std::max(3.1 * bt, 400.0) : std::max(5.4 * bt, 750.0)) + 3000.0);
-                if (real > 1) c += 4000.0 + 8.0 * double(real) * double(M) * double(w.N) / (30.0 * double(sms));
+                double c = double(waves) * (2.0 * slice * (h == 1 ? std::max(3.1 * bt, decode) : std::max(5.4 * bt, 1.85 * decode)) + 3000.0);
+                if (real > 1) c += 8000.0 + 8.0 * double(real) * double(M) * double(w.N) / (30.0 * double(sms));
                 if (c < least) {
                     least = c;
                     best = Plan{h, bt, real, slice, 0, 0};
