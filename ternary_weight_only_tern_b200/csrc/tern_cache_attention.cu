@@ -383,6 +383,7 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
         for (int i = 0; i < kWarps * kSlots; ++i) mbar_init(&sm.full[0][i], 1);
         fence_barrier_init();
     }
+    __syncthreads();            // every warp uses its barriers from its first copy on
     grid_launch_dependents();
     grid_dependency_wait();
 

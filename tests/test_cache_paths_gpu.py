@@ -1,0 +1,31 @@
+"""GPU tests of the 4-bit cache attention's two paths (a CTA per segment where none can be long, an even split with a join where
+some can): what they must share, and what lies around their buffers. The oracle, inputs and tolerance are those of
+test_cache_gpu.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from ternary_weight_only_tern_b200 import api
+from test_cache_gpu import check_attention, cuda, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D,T,G", [(64, 1, 4), (128, 1, 2), (128, 3, 4)])
+def test_short_segments_over_several_waves_of_ctas(D, T, G):
+    """Many more CTAs than the SMs hold at once, most of them of one to three blocks, whose lens and tables the SM has seen
+    before: every launch of them gives the same bits, and no bounded wait runs out."""
+    rng = np.random.default_rng(D + T)
+    lens = [int(n) for n in rng.integers(0, 70, 400)]
+    cache, table, K, V, _, _ = make(rng, lens, 16, 8, D, width=6)
+    q = rng.standard_normal((400, T, 8 * G, D)).astype(np.float16)
+    args = cuda(q), cache, cuda(table), cuda(np.array(lens, np.int32))
+    assert cache.workspace_bytes(400, T, 8 * G, 6) == 0                  # nothing is split
+    first = api.cache_attention(*args)
+    again = [api.cache_attention(*args) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, first) for o in again)
+    check_attention(first.cpu().numpy(), q, K, V, lens, [T] * 400, D**-0.5, 0, 0)
+    from ternary_weight_only_tern_b200 import _lib
+    assert _lib.load().tern_device_status(api._stream()) == 0
