@@ -633,17 +633,26 @@ class PagedCache:
     """Keys and values of past tokens in 4 bits, in pages (struct tern_cache): pool uint8
     [pages, kv_heads, page / 16, 18 head_dim]. Which page holds which tokens of which sequence is said by
     the table of each call, int32 [B, width]: sequence b's token t is in page table[b, t // page], at t % page;
-    an entry outside the pool is no page."""
+    an entry outside the pool is no page. Another pool can be assigned (a larger one, say): the cache then has its sizes,
+    and calls captured before go on with the pool that they were captured with."""
 
     def __init__(self, pool: torch.Tensor):
-        _need(pool, torch.uint8, "pool", ndim=4)
-        self.pages, self.kv_heads, blocks, unit = pool.shape
-        if unit not in (18 * 64, 18 * 128) or not pool.numel():
+        self.pool = pool
+
+    def __setattr__(self, name, value):
+        # another pool brings its sizes, its descriptor and workspace sizes of its own; they cannot be assigned apart from it
+        if name in ("pages", "page", "kv_heads", "head_dim", "_c", "_ref", "_dev", "_ws"):
+            raise AttributeError(f"{name} cannot be assigned: a cache has the sizes of its pool")
+        if name != "pool":
+            self.__dict__[name] = value
+            return
+        _need(value, torch.uint8, "pool", ndim=4)
+        pages, kv_heads, blocks, unit = value.shape
+        if unit not in (18 * 64, 18 * 128) or not value.numel():
             raise ValueError("pool must have shape (pages, kv_heads, page / 16, 18 head_dim), head_dim 64 or 128")
-        self.pool, self.page, self.head_dim = pool, 16 * blocks, unit // 18
-        self._c = _lib.TernCacheC(pool.data_ptr(), self.pages, self.page, self.kv_heads, self.head_dim)
-        self._ref, self._dev = ctypes.byref(self._c), pool.get_device()
-        self._ws = {}
+        c = _lib.TernCacheC(value.data_ptr(), pages, 16 * blocks, kv_heads, unit // 18)
+        self.__dict__.update(pool=value, pages=pages, page=16 * blocks, kv_heads=kv_heads, head_dim=unit // 18, _c=c,
+                             _ref=ctypes.byref(c), _dev=value.get_device(), _ws={})
 
     def __reduce__(self):
         return type(self), (self.pool,)

@@ -1,0 +1,68 @@
+"""Host-side tests of the 4-bit operators' Python objects: what a changed field of a cache or a weight leads to. The tensors are
+CPU ones whose missing device is let through, so that the descriptors can be looked at without a GPU; no call is made."""
+
+import copy
+import pickle
+
+import pytest
+import torch
+
+from ternary_weight_only_tern_b200 import api
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """The binding's check of a tensor without its device."""
+    def need(t, dtype, name, ndim=2):
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+            raise TypeError(name)
+        if t.dim() != ndim or not t.is_contiguous():
+            raise ValueError(name)
+    monkeypatch.setattr(api, "_need", need)
+
+
+def pool(pages=3, heads=2, blocks=4, D=64):
+    return torch.zeros((pages, heads, blocks, 18 * D), dtype=torch.uint8)
+
+
+def described(cache):
+    c = cache._c
+    return c.pool, c.pages, c.page, c.kv_heads, c.head_dim
+
+
+def test_another_pool_takes_the_place_of_the_first(on_cpu):
+    cache = api.PagedCache(pool())
+    cache._ws[(1, 1, 4, 9, 0, 0)] = 123                  # a size that was asked for
+    for p, sizes in ((pool(pages=7), (7, 64, 2, 64)), (pool(heads=5, blocks=1, D=128), (3, 16, 5, 128))):
+        cache.pool = p
+        assert described(cache) == (p.data_ptr(), *sizes)
+        assert (cache.pages, cache.page, cache.kv_heads, cache.head_dim) == sizes
+        assert cache.pool is p and cache.nbytes() == p.numel() and not cache._ws
+        assert cache._ref._obj is cache._c               # the reference that calls pass
+
+
+def test_a_pool_that_cannot_be_one_is_refused_and_changes_nothing(on_cpu):
+    p = pool()
+    cache = api.PagedCache(p)
+    before = described(cache)
+    for bad, error in ((pool(D=96), ValueError), (pool()[:0], ValueError), (pool().half(), TypeError), (pool()[0], ValueError),
+                       (pool(D=128)[..., ::2], ValueError), (None, TypeError)):
+        with pytest.raises(error):
+            cache.pool = bad
+        assert described(cache) == before and cache.pool is p
+
+
+@pytest.mark.parametrize("name", ["pages", "page", "kv_heads", "head_dim", "_c"])
+def test_the_sizes_are_the_pools(on_cpu, name):
+    cache = api.PagedCache(pool())
+    with pytest.raises(AttributeError, match=name):
+        setattr(cache, name, 4)
+    assert cache.kv_heads == 2
+    cache.layer = 7                                      # a user's own
+    assert cache.layer == 7
+
+
+def test_a_copy_of_a_cache_describes_its_own_pool(on_cpu):
+    cache = api.PagedCache(pool())
+    for twin in (copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
+        assert twin.pool.data_ptr() != cache.pool.data_ptr() and twin._c.pool == twin.pool.data_ptr()
