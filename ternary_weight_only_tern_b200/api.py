@@ -469,7 +469,7 @@ class NibWeight:
     mu: torch.Tensor | None = None   # float16 as scale, or None
     static: bool = False     # weights not written by queued work: nib_linear may read them early
 
-    def __post_init__(self):
+    def _check(self):
         _nib_check_shape(self.N, self.K, self.group)
         strips = -(-self.N // 16)
         for t, dt, name, shape in ((self.codes, torch.int32, "codes", (strips, self.K // GROUP, 256)),
@@ -482,20 +482,26 @@ class NibWeight:
                 raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
             if t.device != self.codes.device:
                 raise ValueError("codes, scale and mu must share one device")
+        self.__dict__["_sound"] = True
+
+    __post_init__ = _check
 
     @property
     def device(self) -> torch.device:
         return self.codes.device
 
     def __setattr__(self, name, value):
-        # a changed field drops what is remembered of the weight
+        # a changed field drops what is remembered of the weight, and its fields are held to each other at the next use
         self.__dict__[name] = value
         self.__dict__["_seen"] = None
+        self.__dict__["_sound"] = False
 
     def _known(self) -> tuple:
         """(C descriptor, reference to it, device number, workspace bytes by M), remembered until a field changes."""
         k = self.__dict__.get("_seen")
         if k is None:
+            if not self.__dict__.get("_sound"):
+                self._check()
             c = _lib.TernNibWeightC(self.N, self.K, self.group, _lib.WEIGHT_STATIC if self.static else 0,
                                     self.codes.data_ptr(), self.scale.data_ptr(),
                                     self.mu.data_ptr() if self.mu is not None else None)
@@ -504,7 +510,7 @@ class NibWeight:
 
     def __getstate__(self):
         # a copy has tensors, and so a descriptor, of its own
-        return {k: v for k, v in self.__dict__.items() if k != "_seen"}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_seen", "_sound")}
 
     def c_struct(self) -> _lib.TernNibWeightC:
         return self._known()[0]
@@ -527,7 +533,7 @@ def _nib_empty(N: int, K: int, group: int, offset: bool, like: torch.Tensor) -> 
     scale = like.new_empty((strips, K // group, 16), dtype=_F16)
     w = NibWeight.__new__(NibWeight)       # of the right shapes by construction
     w.__dict__.update(N=N, K=K, group=group, codes=like.new_empty((strips, K // GROUP, 256), dtype=_I32), scale=scale,
-                      mu=torch.empty_like(scale) if offset else None, static=False)
+                      mu=torch.empty_like(scale) if offset else None, static=False, _sound=True)
     return w
 
 

@@ -66,3 +66,50 @@ def test_a_copy_of_a_cache_describes_its_own_pool(on_cpu):
     cache = api.PagedCache(pool())
     for twin in (copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
         assert twin.pool.data_ptr() != cache.pool.data_ptr() and twin._c.pool == twin.pool.data_ptr()
+
+
+def weight(N=40, K=256, group=64, offset=True):
+    strips = -(-N // 16)
+    half = lambda: torch.zeros((strips, K // group, 16), dtype=torch.float16)  # noqa: E731
+    return api.NibWeight(N, K, group, torch.zeros((strips, K // 128, 256), dtype=torch.int32), half(), half() if offset else None)
+
+
+def test_a_changed_field_reaches_the_descriptor(on_cpu):
+    w = weight()
+    first = w.c_struct()
+    assert w.c_struct() is first                         # remembered
+    w.codes = torch.ones_like(w.codes)
+    assert w.c_struct().codes == w.codes.data_ptr()
+    w.mu = None
+    assert not w.c_struct().mu
+    w.static = True
+    assert w.c_struct().flags == 1
+    w.N = 48                                             # as many strips
+    assert w.c_struct().N == 48
+
+
+@pytest.mark.parametrize("name,value,error", [
+    ("N", 49, ValueError), ("K", 384, ValueError), ("K", 200, ValueError), ("group", 128, ValueError), ("group", 16, ValueError), ("N", 0, ValueError),
+    ("codes", torch.zeros((2, 2, 256), dtype=torch.int32), ValueError), ("codes", torch.zeros((3, 2, 256), dtype=torch.uint8), TypeError),
+    ("scale", torch.zeros((3, 2, 16), dtype=torch.float16), ValueError), ("scale", None, TypeError),
+    ("scale", torch.zeros((3, 16, 4), dtype=torch.float16).transpose(1, 2), ValueError),
+    ("mu", torch.zeros((3, 4, 16), dtype=torch.float32), TypeError)])
+def test_a_field_that_does_not_fit_is_refused_at_the_next_use(on_cpu, name, value, error):
+    """Sizes and tensors are assigned one after another, so they are held to each other when the weight is used."""
+    w = weight()
+    w.c_struct()
+    good = getattr(w, name)
+    setattr(w, name, value)
+    for _ in range(2):
+        with pytest.raises(error):
+            w.c_struct()
+    setattr(w, name, good)
+    w.c_struct()
+
+
+def test_a_weight_made_of_right_shapes_is_checked_again_once_changed(on_cpu):
+    w = api._nib_empty(40, 256, 64, True, torch.zeros(1))
+    w.c_struct()
+    w.N = 64
+    with pytest.raises(ValueError, match="codes"):
+        w.c_struct()
