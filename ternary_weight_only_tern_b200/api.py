@@ -441,6 +441,13 @@ def _at(t: torch.Tensor, dtype, name: str, ndim: int, dev: int) -> int:
     return t.data_ptr()
 
 
+def _device_of(t, name: str) -> int:
+    """The tensor's device number (-1: not on a GPU)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
 def _scratch(workspace: torch.Tensor | None, need: int, like: torch.Tensor) -> tuple:
     """(tensor, bytes): the caller's workspace where it is large enough, else one of the call's own."""
     if workspace is not None:
@@ -520,6 +527,12 @@ class NibWeight:
         return sum(t.numel() * t.element_size() for t in (self.codes, self.scale, self.mu) if t is not None)
 
 
+def _nib_known(w) -> tuple:
+    if not isinstance(w, NibWeight):
+        raise TypeError(f"w must be a NibWeight, got {type(w).__name__}")
+    return w._known()
+
+
 def _nib_check_shape(N: int, K: int, group: int):
     if group not in NIB_GROUPS:
         raise ValueError(f"group must be one of {NIB_GROUPS}, got {group}")
@@ -539,7 +552,7 @@ def _nib_empty(N: int, K: int, group: int, offset: bool, like: torch.Tensor) -> 
 
 def nib_fit(W: torch.Tensor, group: int = GROUP, offset: bool = True) -> NibWeight:
     """Dense fp16 W [N, K] -> 4-bit weight by tern_nib_fit, with a per-group offset or symmetric."""
-    dev = W.get_device()
+    dev = _device_of(W, "W")
     at = _at(W, _F16, "W", 2, dev)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -555,7 +568,7 @@ def nib_fit(W: torch.Tensor, group: int = GROUP, offset: bool = True) -> NibWeig
 
 def nib_pack(codes: torch.Tensor, scale: torch.Tensor, mu: torch.Tensor | None = None) -> NibWeight:
     """Row-major codes uint8 [N, K] in 0 .. 15 with scale (and mu) fp16 [N, K/group] -> 4-bit weight."""
-    dev = codes.get_device()
+    dev = _device_of(codes, "codes")
     _at(codes, torch.uint8, "codes", 2, dev)
     N, K = codes.shape
     for t, name in ((scale, "scale"), (mu, "mu")):
@@ -574,7 +587,7 @@ def nib_pack(codes: torch.Tensor, scale: torch.Tensor, mu: torch.Tensor | None =
 
 def nib_dequant(w: NibWeight, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp16 W [N, K] of a 4-bit weight."""
-    _, ref, dev, _ = w._known()
+    _, ref, dev, _ = _nib_known(w)
     if dev != _current_device():
         with torch.cuda.device(dev):
             return nib_dequant(w, out)
@@ -593,7 +606,7 @@ def nib_dequant(w: NibWeight, out: torch.Tensor | None = None) -> torch.Tensor:
 
 def nib_workspace_bytes(w: NibWeight, M: int) -> int:
     """tern_nib_linear_workspace_bytes, remembered per weight and M."""
-    _, ref, dev, sizes = w._known()
+    _, ref, dev, sizes = _nib_known(w)
     n = sizes.get(M)
     if n is None:
         with torch.cuda.device(dev):
@@ -604,8 +617,7 @@ def nib_workspace_bytes(w: NibWeight, M: int) -> int:
 def nib_linear(x: torch.Tensor, w: NibWeight, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y [M, N] = x [M, K] . W^T for a 4-bit W (fp16 in, fp32 accumulation, fp16 out)."""
-    _need(x, _F16, "x") if not isinstance(w, NibWeight) else None
-    _, ref, dev, sizes = w._known()
+    _, ref, dev, sizes = _nib_known(w)
     at = _at(x, _F16, "x", 2, dev)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -687,6 +699,12 @@ class PagedCache:
         return n
 
 
+def _cache_device(cache) -> int:
+    if not isinstance(cache, PagedCache):
+        raise TypeError(f"cache must be a PagedCache, got {type(cache).__name__}")
+    return cache._dev
+
+
 def _per_sequence(t: torch.Tensor | None, name: str, B: int, dev: int):
     """Address of an int32 [B] tensor, or None."""
     if t is None:
@@ -709,7 +727,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, table: tor
                  counts: torch.Tensor | None = None) -> None:
     """Quantises k, v fp16 [B, T, kv_heads, head_dim] into the cache: token t < counts[b] (T without
     counts) of sequence b becomes its token start[b] + t."""
-    dev = cache._dev
+    dev = _cache_device(cache)
     ka, va = _at(k, _F16, "k", 4, dev), _at(v, _F16, "v", 4, dev)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -728,12 +746,13 @@ def cache_read(cache: PagedCache, table: torch.Tensor, start: torch.Tensor, T: i
                counts: torch.Tensor | None = None, out: tuple | None = None) -> tuple:
     """(k, v) fp16 [B, T, kv_heads, head_dim]: the cached tokens start[b] + t, zeros at t >= counts[b] and
     where there is no page."""
-    dev = cache._dev
+    dev = _cache_device(cache)
+    _device_of(table, "table")
     if dev != _current_device():
         with torch.cuda.device(dev):
             return cache_read(cache, table, start, T, counts, out)
-    B = table.shape[0]
-    ta, width = _table(table, B, dev)
+    ta = _at(table, _I32, "table", 2, dev)
+    B, width = table.shape
     shape = (B, T, cache.kv_heads, cache.head_dim)
     if out is None:
         k = table.new_empty(shape, dtype=_F16)
@@ -759,7 +778,7 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, len
     sequence's lens[b] cached tokens, of which its queries are the last counts[b] (T without counts;
     rows behind them are left as they were). Causal; with window > 0 a query sees the last `window` tokens up to its
     own and the first `sinks`. scale: 1 / sqrt(head_dim) by default."""
-    dev = cache._dev
+    dev = _cache_device(cache)
     qa = _at(q, _F16, "q", 4, dev)
     if dev != _current_device():
         with torch.cuda.device(dev):

@@ -113,3 +113,35 @@ def test_a_weight_made_of_right_shapes_is_checked_again_once_changed(on_cpu):
     w.N = 64
     with pytest.raises(ValueError, match="codes"):
         w.c_struct()
+
+
+def other_weight():
+    t = torch.zeros
+    return api.TernWeight(16, 128, t((16, 8), dtype=torch.int32), t((16, 1), dtype=torch.float16), t(0, dtype=torch.int32),
+                          t(16, dtype=torch.int32), t((0, 8), dtype=torch.int32), t((0, 1), dtype=torch.float16))
+
+
+@pytest.mark.parametrize("w", [None, 3, torch.zeros((16, 128), dtype=torch.float16), other_weight()], ids=["None", "number", "dense", "ternary"])
+def test_what_is_no_nib_weight_is_refused_by_name(w):
+    x = torch.zeros((1, 128), dtype=torch.float16)
+    for call in (lambda: api.nib_linear(x, w), lambda: api.nib_dequant(w), lambda: api.nib_workspace_bytes(w, 1)):
+        with pytest.raises(TypeError, match="NibWeight"):
+            call()
+
+
+@pytest.mark.parametrize("cache", [None, pool(), weight], ids=["None", "pool", "function"])
+def test_what_is_no_cache_is_refused_by_name(cache):
+    x, i = torch.zeros((1, 1, 2, 64), dtype=torch.float16), torch.zeros((1, 1), dtype=torch.int32)
+    for call in (lambda: api.cache_append(cache, x, x, i, i[0]), lambda: api.cache_read(cache, i, i[0], 1),
+                 lambda: api.cache_attention(x, cache, i, i[0])):
+        with pytest.raises(TypeError, match="PagedCache"):
+            call()
+
+
+@pytest.mark.parametrize("t", [None, [1, 2], 3.0])
+def test_what_is_no_tensor_is_refused_as_one(on_cpu, t):
+    cache, i = api.PagedCache(pool()), torch.zeros((1, 1), dtype=torch.int32)
+    for call in (lambda: api.nib_fit(t), lambda: api.nib_pack(t, t), lambda: api.nib_linear(t, weight()), lambda: api.cache_append(cache, t, t, i, i[0]),
+                 lambda: api.cache_read(cache, t, i[0], 1), lambda: api.cache_attention(t, cache, i, i[0])):
+        with pytest.raises(TypeError):
+            call()
