@@ -53,6 +53,7 @@ constexpr int setup_of(int nt) { return nt == 1 ? 16 : 24; }
 constexpr int kMinUnits = 8;               // cost per CTA at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxScale = 1e4f;          // keeps scale q k of finite inputs finite
+constexpr float kLift = 7.f, kSlack = 8.f; // a probability counts 2^kLift at the running maximum, and up to 2^kSlack more (raise)
 
 struct Desc {               // a (sequence, kv head, row tile) in pieces: where the first lies
     int b, h, rt, pieces;   // pieces < 2: nothing to join
@@ -69,7 +70,7 @@ struct Args {
     int setup;                  // cost of a segment beyond its units
     int B, T, heads, G, RT;     // G = heads per kv head, RT = row tiles
     float scale;                // of the exponents (to base 2), > 0
-    float slack;                // 8 / scale
+    float slack;                // kSlack / scale
     uint32_t sign;              // turns the queries' signs where the caller's scale is negative
     Desc* desc;                 // [ndesc]: by (sequence, head, tile) where these are fewer than the CTAs, else by CTA
     int ndesc;
@@ -144,7 +145,7 @@ __device__ __forceinline__ float ex2(float x) {
 template <int D, int NT>
 struct State {
     float m[NT][2], l[NT][2];   // of rows 2 q and 2 q + 1 of each 8: maximum of q k, sum of this lane's tokens alone
-    float base[NT][2];          // what the exponents are taken less of: scale m, or 0 while there is none
+    float base[NT][2];          // what the exponents are taken less of: scale m - kLift, or 0 while there is none
     float o[NT][D / 16][4];
 };
 
@@ -226,8 +227,10 @@ __device__ __forceinline__ void hide(uint8_t* u, int j0, bool there, const int (
     }
 }
 
-// The running maximum of a row moves only when some token is 2^8 above it (a probability may then be up to 2^8,
-// well inside fp16): seldom, so the reduction over the 8 lanes of a column is not paid per block.
+// The running maximum of a row moves only when some token is 2^kSlack above it: seldom, so the reduction over the 8 lanes of
+// a column is not paid per block. A probability counts 2^kLift at the maximum, so that P uses fp16's range up to 2^15: one of 2^-21
+// of the maximum still has all its bits, and none above 2^-32 of it is lost. (Where a first token takes nearly all of the mass and
+// has a small V, the result is left to such tokens.)
 template <int D, int NT, int kBlocks>
 __device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Args& a, State<D, NT>& st) {
     bool up = false;
@@ -252,7 +255,7 @@ __device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Ar
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float f = m > st.m[t][c] ? ex2((st.m[t][c] - m) * a.scale) : 1.f;
             st.m[t][c] = m;
-            st.base[t][c] = m == -INFINITY ? 0.f : m * a.scale;
+            st.base[t][c] = m == -INFINITY ? 0.f : fmaf(m, a.scale, -kLift);
             st.l[t][c] *= f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -841,7 +844,7 @@ extern "C" tern_status tern_cache_attention(const tern_cache* cache, const tern_
     a.heads = int(heads);
     a.G = int(heads / cache->kv_heads);
     a.scale = fmaxf(fabsf(scale) * kLog2e, 1e-30f);    // zero is as good as 1e-30
-    a.slack = 8.f / a.scale;
+    a.slack = kSlack / a.scale;
     a.sign = scale < 0.f ? 0x80008000u : 0u;
     cudaStream_t cs = as_cuda(stream);
     if (tiles_of(T, a.G) == 1)

@@ -51,3 +51,41 @@ def test_a_cache_goes_on_in_a_larger_pool():
         K[b], V[b] = (np.concatenate([X[b], no.cache_values(*no.cache_quantise(x[b]))]) for X, x in ((K, k), (V, v)))
     o = api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array(lens, np.int32) + 10)).cpu().numpy()
     check_attention(o, q, K, V, [50, 35], [1, 1], 0.125, 0, 0)
+
+
+def first_token_above(n, powers, D, scale, rng):
+    """K, V of n tokens, one kv head, and a query of 4 heads: token 0 lies about `powers` powers of two above the others and its V is
+    zero, so that the others, all about alike, are the whole result."""
+    q = rng.standard_normal(D)
+    k = rng.standard_normal((1, n, 1, D)) * 0.1
+    k[0, 0, 0] = q * powers * np.log(2) / (scale * (q @ q))
+    v = 4 + rng.standard_normal((1, n, 1, D))
+    v[0, 0] = 0
+    return k.astype(np.float16), v.astype(np.float16), np.repeat(q[None, None, None], 4, 2).astype(np.float16)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,powers", [(9, 14), (9, 19), (30, 14), (30, 17), (30, 19), (30, 26), (30, 30), (600, 14), (600, 19), (600, 26), (5000, 19), (5000, 26),
+                                      (131072, 19), (131072, 26)])
+def test_tokens_far_below_the_first_one_keep_their_bits(n, powers, D):
+    """Tolerance: a probability counts 2^7 at the maximum, so one of at least 2^-21 of it is a normal fp16 number and rounded by
+    2^-11 of itself, as are V and the result; below that each is off by up to 2^-25 2^-7 of the maximum's. A score is off by at most
+    D 2^-22 |q| |k| scale. (At 2^7 less, those of 2^-26 would all be zeros, and so would the result.)"""
+    rng = np.random.default_rng(n + powers)
+    scale, page = D**-0.5, 64
+    k, v, q = first_token_above(n, powers, D, scale, rng)
+    cache = api.PagedCache.empty(-(-n // page), page, 1, D)
+    table = np.arange(-(-n // page), dtype=np.int32)[None]
+    api.cache_append(cache, cuda(k), cuda(v), cuda(table), cuda(np.zeros(1, np.int32)))
+    K, V = (no.cache_values(*no.cache_quantise(x[0])) for x in (k, v))
+    o = api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array([n], np.int32))).cpu().numpy().astype(np.float64)[0, 0]
+    s = scale * (K[:, 0] @ q[0, 0, 0].astype(np.float64))
+    p = np.exp(s - s[0])
+    low = np.count_nonzero(p < 2.0**-21)
+    assert p[1:].max() < 2.0**(2 - powers)
+    p /= p.sum()
+    ref, mass = p @ V[:, 0], p @ np.abs(V[:, 0])
+    qk = np.linalg.norm(q[0, 0, 0].astype(np.float64)) * np.linalg.norm(K[:, 0], axis=-1).max()
+    tol = 2.0**-11 * np.abs(ref) + 2.0**-25 + (2 * 2.0**-11 + 2 * D * 2.0**-22 * qk * scale) * mass + low * 2.0**-32 * np.abs(V).max()
+    err = np.abs(o - ref)
+    assert (err <= tol).all(), f"{np.max(err / tol):.3g} of the tolerance"
