@@ -54,6 +54,7 @@ constexpr int kMinUnits = 8;               // cost per CTA at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxScale = 1e4f;          // keeps scale q k of finite inputs finite
 constexpr float kLift = 7.f, kSlack = 8.f; // a probability counts 2^kLift at the running maximum, and up to 2^kSlack more (raise)
+constexpr float kNothing = -3.4e38f;       // the maximum of no scores: below any score, and finite, so that no difference is NaN
 
 struct Desc {               // a (sequence, kv head, row tile) in pieces: where the first lies
     int b, h, rt, pieces;   // pieces < 2: nothing to join
@@ -145,7 +146,6 @@ __device__ __forceinline__ float ex2(float x) {
 template <int D, int NT>
 struct State {
     float m[NT][2], l[NT][2];   // of rows 2 q and 2 q + 1 of each 8: maximum of q k, sum of this lane's tokens alone
-    float base[NT][2];          // what the exponents are taken less of: scale m - kLift, or 0 while there is none
     float o[NT][D / 16][4];
 };
 
@@ -241,7 +241,7 @@ __device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Ar
             float top = fmaxf(s[0][t][c], s[0][t][2 + c]);
 #pragma unroll
             for (int k = 1; k < kBlocks; ++k) top = fmaxf(top, fmaxf(s[k][t][c], s[k][t][2 + c]));
-            up |= top > st.m[t][c] + a.slack;
+            up |= top - st.m[t][c] > a.slack;
         }
     if (!__any_sync(0xffffffffu, up)) return;
 #pragma unroll
@@ -255,7 +255,6 @@ __device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Ar
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float f = m > st.m[t][c] ? ex2((st.m[t][c] - m) * a.scale) : 1.f;
             st.m[t][c] = m;
-            st.base[t][c] = m == -INFINITY ? 0.f : fmaf(m, a.scale, -kLift);
             st.l[t][c] *= f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -265,7 +264,8 @@ __device__ __forceinline__ void raise(const float (&s)[kBlocks][NT][4], const Ar
         }
 }
 
-// A block's probabilities, and its V into O^T.
+// A block's probabilities, and its V into O^T. A score's distance to the maximum is taken before it is scaled: the product of
+// a large score is off by more than the distance (scores past 2^28 gave infinities).
 template <int D, int NT>
 __device__ __forceinline__ void add_values(const uint8_t* u, const float (&s)[NT][4], const Args& a, State<D, NT>& st) {
     constexpr int W = D / 32, NG = D / kGrp;
@@ -275,7 +275,7 @@ __device__ __forceinline__ void add_values(const uint8_t* u, const float (&s)[NT
     for (int t = 0; t < NT; ++t) {
         float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[t][i], a.scale, -st.base[t][i & 1]));
+        for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[t][i] - st.m[t][i & 1], a.scale, kLift));
         st.l[t][0] += p[0] + p[2];
         st.l[t][1] += p[1] + p[3];
         b0[t] = transposed(pack_h2(p[0], p[1]));
@@ -534,8 +534,8 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
         State<D, NT> st;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            st.m[t][0] = st.m[t][1] = -INFINITY;
-            st.l[t][0] = st.l[t][1] = st.base[t][0] = st.base[t][1] = 0.f;
+            st.m[t][0] = st.m[t][1] = kNothing;
+            st.l[t][0] = st.l[t][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) st.o[t][i][0] = st.o[t][i][1] = st.o[t][i][2] = st.o[t][i][3] = 0.f;
         }
@@ -585,16 +585,16 @@ __global__ void __launch_bounds__((kDirect ? kDirect : kSplitWarps) * 32, reside
         __syncthreads();
         if (threadIdx.x < kRows) {      // each warp's factor of a row, in place of its maximum; the row's sum
             const int r = threadIdx.x;
-            float top = -INFINITY, l = 0.f;
+            float top = kNothing, l = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.m[w][r]);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = top == -INFINITY ? 1.f : ex2((sm.m[w][r] - top) * a.scale);
+                const float f = ex2((sm.m[w][r] - top) * a.scale);
                 l += f * sm.l[w][r];
                 sm.m[w][r] = f;
             }
-            sm.top[r] = top * a.scale;
+            sm.top[r] = top;
             sm.l[0][r] = l;
         }
         float* wo = reinterpret_cast<float*>(ring);
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
     const int64_t size = part_floats<D, NT>();
     const float* base = a.part + int64_t(ds.cta) * 2 * size + r * stride;
     const int d = threadIdx.x % D, part = threadIdx.x / D;
-    float m = -INFINITY, l = 0.f, o = 0.f;
+    float m = kNothing, l = 0.f, o = 0.f;
     for (int p0 = part; p0 < ds.pieces; p0 += kBatch * kPar) {
         float pm[kBatch], pl[kBatch], po[kBatch];
 #pragma unroll
@@ -677,19 +677,19 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
             const int p = p0 + i * kPar;
             const float* from = base + (p == 0 ? size : 2 * size * p);
             const bool there = p < ds.pieces;
-            pm[i] = there ? from[D] : -INFINITY;
+            pm[i] = there ? from[D] : kNothing;
             pl[i] = there ? from[D + 1] : 0.f;
             po[i] = there ? from[d] : 0.f;
         }
         float top = m;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) top = fmaxf(top, pm[i]);
-        const float base2 = top == -INFINITY ? 0.f : top, f = ex2(m - base2);
+        const float f = ex2((m - top) * a.scale);
         l *= f;
         o *= f;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const float e = ex2(pm[i] - base2);
+            const float e = ex2((pm[i] - top) * a.scale);
             l += e * pl[i];
             o += e * po[i];
         }
@@ -702,14 +702,13 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const Args a) {
     }
     __syncthreads();
     if (part) return;
-    float top = -INFINITY;
+    float top = kNothing;
 #pragma unroll
     for (int i = 0; i < kPar; ++i) top = fmaxf(top, sm_m[i]);
-    const float base2 = top == -INFINITY ? 0.f : top;
     l = o = 0.f;
 #pragma unroll
     for (int i = 0; i < kPar; ++i) {
-        const float e = ex2(sm_m[i] - base2);
+        const float e = ex2((sm_m[i] - top) * a.scale);
         l += e * sm_l[i];
         o += e * sm_o[i][d];
     }

@@ -89,3 +89,31 @@ def test_tokens_far_below_the_first_one_keep_their_bits(n, powers, D):
     tol = 2.0**-11 * np.abs(ref) + 2.0**-25 + (2 * 2.0**-11 + 2 * D * 2.0**-22 * qk * scale) * mass + low * 2.0**-32 * np.abs(V).max()
     err = np.abs(o - ref)
     assert (err <= tol).all(), f"{np.max(err / tol):.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("scale", [128**-0.5, -(128**-0.5), 1e4, -7.0])
+@pytest.mark.parametrize("n", [40, 700, 6000])
+def test_scores_of_any_size_leave_a_result(n, scale):
+    """Queries and keys near the ends of fp16's range: scores to base 2 of up to 1e9 (1e14 with the largest scale), whose last bits
+    count far more than 1. One token is above all others by much more than a score's error (D 2^-22 |q| |k| scale: 2^-15 of the
+    largest score), so each query's result is that token's V, rounded to fp16 for the product and so exact here."""
+    rng = np.random.default_rng(n)
+    D, heads, page = 128, 24, 64
+    u = np.where(rng.random(D) < 0.5, -1.0, 1.0)
+    c = rng.permutation(np.linspace(-1, 1, n))           # of the key along u; steps of at least 2^-12
+    k = (c[:, None] * u * 60000.0).astype(np.float16)
+    v = rng.integers(-50, 50, (n, D)).astype(np.float16)
+    q = (np.where(np.arange(heads) % 2, 1.0, -1.0)[:, None] * np.ldexp(1000.0, -(np.arange(heads) // 2))[:, None] * u).astype(np.float16)
+    cache = api.PagedCache.empty(-(-n // page), page, 1, D)
+    table = np.arange(-(-n // page), dtype=np.int32)[None]
+    api.cache_append(cache, cuda(k[None, :, None]), cuda(v[None, :, None]), cuda(table), cuda(np.zeros(1, np.int32)))
+    K, V = (no.cache_values(*no.cache_quantise(x)) for x in (k, v))
+    s = scale * (q.astype(np.float64) @ K.T)
+    best = s.argmax(1)
+    two = np.sort(s, 1)[:, -2:]
+    error = D * 2.0**-22 * np.linalg.norm(q.astype(np.float64), axis=1) * np.linalg.norm(K, axis=1).max() * abs(scale)
+    clear = two[:, 1] - two[:, 0] > 2 * error + 40       # the second token's share is below e^-40
+    assert clear.sum() >= 8 and np.abs(s).max() > 3e8 / 1.5
+    o = api.cache_attention(cuda(q[None, None]), cache, cuda(table), cuda(np.array([n], np.int32)), scale=scale).cpu().numpy()[0, 0]
+    assert np.isfinite(o).all()
+    assert np.array_equal(o[clear], V.astype(np.float16)[best[clear]])
