@@ -326,14 +326,15 @@ tern_status tern_nib_fit(const tern_half* W, int64_t N, int64_t K, int32_t group
 tern_status tern_nib_pack(const uint8_t* c, const tern_half* s, const tern_half* m, int64_t N, int64_t K,
                           int32_t group, uint32_t* codes, tern_half* scale, tern_half* mu, tern_stream stream);
 
-/* out [N, K] (device) = fp16 of W, each weight rounded once. Asynchronous on `stream`.   */
+/* out [N, K] (device) = fp16 of W, each weight rounded once (infinite past 65504). Asynchronous on `stream`. */
 tern_status tern_nib_dequant(const tern_nib_weight* w, tern_half* out, tern_stream stream);
 
 /* Bytes of workspace tern_nib_linear needs for this weight and batch size (0 if none).  */
 size_t tern_nib_linear_workspace_bytes(const tern_nib_weight* w, int64_t M);
 
-/* y [M, N] = x [M, K] . W^T (x, y device, fp16, row-major), fp32 accumulation, one rounding to
- * fp16. 0 <= M <= 2^22 (0 is a no-op). x and y must not overlap. Workspace rule, streams and capture
+/* y [M, N] = x [M, K] . W^T (x, y device, fp16, row-major), fp32 accumulation, y rounded to fp16 once. Up to 16
+ * tokens W enters as it is; past them as tern_nib_dequant gives it, each weight rounded to fp16 (and infinite
+ * past 65504). 0 <= M <= 2^22 (0 is a no-op). x and y must not overlap. Workspace rule, streams and capture
  * as for tern_linear. An infinity in x makes its token's y infinite or NaN.               */
 tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half* x, int64_t M, tern_half* y, void* workspace,
                             size_t workspace_bytes, tern_stream stream);

@@ -616,7 +616,8 @@ def nib_workspace_bytes(w: NibWeight, M: int) -> int:
 
 def nib_linear(x: torch.Tensor, w: NibWeight, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """y [M, N] = x [M, K] . W^T for a 4-bit W (fp16 in, fp32 accumulation, fp16 out)."""
+    """y [M, N] = x [M, K] . W^T for a 4-bit W (fp16 in, fp32 accumulation, fp16 out). Past 16 tokens W enters as nib_dequant
+    gives it, each weight rounded to fp16."""
     _, ref, dev, sizes = _nib_known(w)
     at = _at(x, _F16, "x", 2, dev)
     if dev != _current_device():
