@@ -117,3 +117,33 @@ def test_scores_of_any_size_leave_a_result(n, scale):
     o = api.cache_attention(cuda(q[None, None]), cache, cuda(table), cuda(np.array([n], np.int32)), scale=scale).cpu().numpy()[0, 0]
     assert np.isfinite(o).all()
     assert np.array_equal(o[clear], V.astype(np.float16)[best[clear]])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Hk,G,T,longest,width,split", [(3, 2, 4, 1, 9000, None, True), (2, 1, 3, 5, 9000, None, True), (3, 2, 2, 64, 3000, None, True),
+                                                          (150, 8, 2, 1, 200, 60, True), (60, 5, 3, 7, 200, 60, True), (40, 3, 4, 1, 200, None, False),
+                                                          (9, 3, 5, 6, 200, None, False)])
+def test_attention_writes_its_rows_and_workspace_alone(B, Hk, G, T, longest, width, split, D):
+    """Fewer and more segments than CTAs, split ones and such with a CTA of their own: a workspace of just the stated bytes (all NaN before)
+    and the output lie between guard bytes, which stay as they are, as do the output's rows behind a sequence's queries."""
+    rng = np.random.default_rng(B + T + D)
+    lens = [longest] + [int(n) for n in rng.integers(0, longest, B - 1)]
+    counts = [T] + [int(n) for n in rng.integers(0, T + 1, B - 1)]
+    cache, table, K, V, _, _ = make(rng, lens, 32, Hk, D, width=width)
+    H, W = Hk * G, table.shape[1]
+    need = cache.workspace_bytes(B, T, H, W)
+    assert (need > 0) == split
+    q = rng.standard_normal((B, T, H, D)).astype(np.float16)
+    n = q.size
+    buf = torch.full((n + 256,), 7.5, dtype=torch.float16, device="cuda")
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws[256:256 + need] = 0xFF
+    out = buf[128:128 + n].view(B, T, H, D)
+    api.cache_attention(cuda(q), cache, cuda(table), cuda(np.array(lens, np.int32)), counts=cuda(np.array(counts, np.int32)), out=out,
+                        workspace=ws[256:256 + need])
+    assert (buf[:128] == 7.5).all() and (buf[128 + n:] == 7.5).all()
+    assert (ws[:256] == 0x5A).all() and (ws[256 + need:] == 0x5A).all()
+    assert not split or (ws[256:256 + need] != 0xFF).any()       # (the workspace given is the one used)
+    o = out.cpu().numpy()
+    assert all((o[b, counts[b]:] == 7.5).all() for b in range(B))
+    check_attention(o, q, K, V, lens, counts, D**-0.5, 0, 0)

@@ -7,7 +7,7 @@ import torch
 
 from oracle import nib_oracle as no
 from ternary_weight_only_tern_b200 import api
-from test_nib_gpu import draw, weight
+from test_nib_gpu import check_product, draw, weight
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,26 @@ def test_weights_past_the_range_of_fp16(M):
         assert not np.isfinite(row).any()
     else:
         assert (np.abs(row - 70008 * 2.0**-12) <= 2.0**-11 * 17.1).all()
+
+
+@pytest.mark.parametrize("M,N,K,group", [(16, 515, 12288, 128), (9, 37, 20480, 32), (2, 50, 65536, 64), (24, 1000, 2560, 64), (40, 130, 9728, 32),
+                                         (300, 260, 4096, 64), (200, 1001, 2560, 128)])
+def test_sums_of_slices_stay_in_their_workspace(M, N, K, group):
+    """Calls that cut K into slices, on both paths: a workspace of just the stated bytes (all NaN before) and the output lie between guard
+    bytes, which stay as they are, and the result is that of a call with buffers of its own."""
+    rng = np.random.default_rng(M + N)
+    c, s, mu = draw(rng, N, K, group, True)
+    w = weight(c, s, mu)
+    need = api.nib_workspace_bytes(w, M)
+    assert need >= 2 * M * N * 4
+    x = torch.from_numpy(rng.standard_normal((M, K), dtype=np.float32).astype(np.float16)).cuda()
+    buf = torch.full((M * N + 256,), 7.5, dtype=torch.float16, device="cuda")
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws[256:256 + need] = 0xFF
+    out = buf[128:128 + M * N].view(M, N)
+    api.nib_linear(x, w, out=out, workspace=ws[256:256 + need])
+    assert (buf[:128] == 7.5).all() and (buf[128 + M * N:] == 7.5).all()
+    assert (ws[:256] == 0x5A).all() and (ws[256 + need:] == 0x5A).all()
+    assert (ws[256:256 + need] != 0xFF).any()              # (the workspace given is the one used)
+    check_product(out.cpu().numpy(), x.cpu().numpy(), no.nib_values(c, s, mu))
+    assert torch.equal(api.nib_linear(x, w), out)
