@@ -355,8 +355,9 @@ tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half* x, int64_
  * Sequence b's token t lies in page table[b, t / page] (table int32 [B, width], device), at t % page. An
  * entry outside 0 .. pages - 1, or a t past the table's width, is no page: nothing is written there,
  * it reads as zeros, and attention does not see it. Pages may be shared by sequences that only
- * read them; two tokens of one tern_cache_append in the same place leave either. In the calls below B and
- * heads are at most 65535, T (but for attention) and width at most 2^24.                  */
+ * read them; two tokens of one tern_cache_append in the same place leave a mixture of their codes, steps and
+ * zeros there, which is neither unless they are equal. Other places are not touched by it. In the calls below
+ * B and heads are at most 65535, T (but for attention) and width at most 2^24.            */
 typedef struct {
     uint8_t* pool;               /* [pages, kv_heads, page / 16, 18 head_dim], device, 16-byte aligned */
     int64_t pages;               /* pages kv_heads page / 16 < 2^31                       */

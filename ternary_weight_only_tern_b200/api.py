@@ -727,7 +727,8 @@ def _table(table: torch.Tensor, B: int, dev: int) -> tuple:
 def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
                  counts: torch.Tensor | None = None) -> None:
     """Quantises k, v fp16 [B, T, kv_heads, head_dim] into the cache: token t < counts[b] (T without
-    counts) of sequence b becomes its token start[b] + t."""
+    counts) of sequence b becomes its token start[b] + t. No two of them may lie in the same place of a page, unless they are
+    equal."""
     dev = _cache_device(cache)
     ka, va = _at(k, _F16, "k", 4, dev), _at(v, _F16, "v", 4, dev)
     if dev != _current_device():

@@ -147,3 +147,25 @@ def test_attention_writes_its_rows_and_workspace_alone(B, Hk, G, T, longest, wid
     o = out.cpu().numpy()
     assert all((o[b, counts[b]:] == 7.5).all() for b in range(B))
     check_attention(o, q, K, V, lens, counts, D**-0.5, 0, 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_two_tokens_in_one_place(D):
+    """Two sequences that share their pages append to the same tokens: where they are equal (a common beginning) nothing is lost, where
+    they are not every code, step and zero is that of one of them, and no other token changes."""
+    rng = np.random.default_rng(D)
+    T, Hk, page = 24, 2, 16
+    k, v = (rng.standard_normal((2, T, Hk, D)).astype(np.float16) for _ in range(2))
+    same = 10
+    k[1, :same], v[1, :same] = k[0, :same], v[0, :same]
+    table, start = cuda(np.array([[1, 2], [1, 2]], np.int32)), cuda(np.full(2, 3, np.int32))
+    caches = [api.PagedCache(torch.full((4, Hk, 1, 18 * D), 0x33, dtype=torch.uint8, device="cuda")) for _ in range(3)]
+    for b in range(2):
+        api.cache_append(caches[b], cuda(k[b:b + 1]), cuda(v[b:b + 1]), table[:1], start[:1])
+    for _ in range(10):
+        api.cache_append(caches[2], cuda(k), cuda(v), table, start)
+        one, two, both = (c.pool.view(torch.int16) for c in caches)
+        assert ((both == one) | (both == two)).all()       # (half words: a token's codes are whole ones)
+        got = api.cache_read(caches[2], table, start, same)
+        want = api.cache_read(caches[0], table, start, same)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
