@@ -344,8 +344,10 @@ tern_status tern_nib_linear(const tern_nib_weight* w, const tern_half* x, int64_
 /* Keys and values of past tokens in 4 bits, in pages (the pages leave attention and its cache in 16
  * bits: "Post-Training Ternarization of Qwen3-4B", section 3.1; next to 2-bit weights the cache is what
  * a decode step reads most). Per token, head and 64 entries of the head: an fp16 step s and an
- * fp16 zero z, value = z + s c, c in 0 .. 15. A page holds `page` tokens of every kv head; per
- * (page, head) it is page / 16 blocks of 16 tokens, 18 head_dim bytes each, D = head_dim:
+ * fp16 zero z, value = z + s c, c in 0 .. 15; values past 65504 (a step rounded up can take the largest one
+ * there) are infinite in fp16, so in tern_cache_read and as V in the attention. A page holds `page` tokens
+ * of every kv head; per (page, head) it is page / 16 blocks of 16 tokens, 18 head_dim bytes each, D =
+ * head_dim:
  *   K codes   8 D bytes: word ((h 8 + g) 4 + q) D / 32 + j: token 8 h + g, entries 32 j + 8 q .. + 7
  *             (nibbles as in tern_nib_weight.codes);
  *   V codes   8 D bytes: word ((h 8 + g) 4 + q) D / 32 + j: tokens 8 h + 2 q (bits 4 p, p = 0 .. 3) and

@@ -169,3 +169,27 @@ def test_two_tokens_in_one_place(D):
         got = api.cache_read(caches[2], table, start, same)
         want = api.cache_read(caches[0], table, start, same)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_values_at_the_end_of_fp16s_range():
+    """A range of -65504 .. 65504 has a step of 8733.9, rounded to 8736: its top is 65536, finite in K's scores (which are in fp32) and
+    infinite where it is turned into fp16."""
+    D, n = 64, 20
+    k = np.zeros((1, n, 1, D), np.float16)
+    k[0, 4, 0, 0], k[0, 4, 0, 1] = 65504, -65504
+    v = np.ones((1, n, 1, D), np.float16)
+    v[0, 4] = 2
+    cache = api.PagedCache.empty(2, 16, 1, D)
+    table, zero = cuda(np.array([[1, 0]], np.int32)), cuda(np.zeros(1, np.int32))
+    api.cache_append(cache, cuda(k), cuda(v), table, zero)
+    K = no.cache_values(*no.cache_quantise(k[0]))
+    got = api.cache_read(cache, table, zero, n)[0][0].cpu().numpy()
+    with np.errstate(over="ignore"):
+        assert K[4, 0, 0] == 65536 and np.array_equal(got, K.astype(np.float16)) and np.isinf(got[4, 0, 0])
+    q = np.zeros((1, 1, 2, D), np.float16)
+    q[0, 0, 0, 0], q[0, 0, 1, 0] = 1, -1                   # all for token 4, and all for the others
+    o = api.cache_attention(cuda(q), cache, table, zero + n).cpu().numpy()[0, 0]
+    assert (o[0] == 2).all() and (o[1] == 1).all()
+    api.cache_append(cache, cuda(v), cuda(k), table, zero)      # as V: the row that sees it all is infinite or NaN there, and there alone
+    o = api.cache_attention(cuda(q), cache, table, zero + n).cpu().numpy()[0, 0]
+    assert not np.isfinite(o[:, 0]).any() and np.isfinite(o[:, 1:]).all()
