@@ -395,7 +395,8 @@ size_t tern_cache_attention_workspace_bytes(const tern_cache* cache, int64_t B, 
  * (T each): sequence b has counts[b] queries (clamped to 0 .. T), query i at token lens[b] - counts[b] +
  * i; rows of o at i >= counts[b] are left as they were. A query at token p sees token j when
  * j <= p, and, with window > 0, j > p - window or j < sinks. One that sees nothing gets zeros. |scale| <= 1e4. Scores,
- * softmax and sums in fp32, the probabilities rounded to fp16 for the product with V, V to fp16 once.
+ * softmax and sums in fp32, the probabilities rounded to fp16 for the product with V (those below 2^-32 of the
+ * largest to zero), V to fp16 once.
  * q and o must not overlap. Workspace rule and capture as for tern_linear.                */
 tern_status tern_cache_attention(const tern_cache* cache, const tern_half* q, int64_t B, int64_t T, int64_t heads,
                                  const int32_t* table, int64_t width, const int32_t* lens, const int32_t* counts,
@@ -436,13 +437,13 @@ tern_status tern_bits_elem(int64_t N, int64_t K, int64_t masked, int64_t nnz2, i
                            tern_bits_report* out);
 
 /* Reports, and clears, the current device's sticky status word for asynchronous work: returns
- * TERN_ERR_TIMEOUT if a tern_linear kernel since the last call gave up a bounded device-side
- * wait (its output is then undefined), TERN_ERR_BOUNDS if, in a TERN_DEBUG build, one of its
+ * TERN_ERR_TIMEOUT if a kernel with bounded device-side waits (tern_linear's, tern_nib_linear's,
+ * tern_cache_attention's) since the last call gave up one (its output is then undefined), TERN_ERR_BOUNDS if, in a TERN_DEBUG build, one of its
  * device-side bounds checks failed (that access was skipped; the output is undefined), else
  * TERN_OK. Synchronous on `stream`.                                                       */
 tern_status tern_device_status(tern_stream stream);
 
-/* 1 for a TERN_DEBUG build (libtern_debug.so: the decode kernels check their shared- and global-
+/* 1 for a TERN_DEBUG build (libtern_debug.so: the ternary decode kernels check their shared- and global-
  * memory indices before each access and report a failure through tern_device_status instead of
  * faulting), 0 for the release build. No counterpart on the pages: a test aid.            */
 int tern_debug_build(void);

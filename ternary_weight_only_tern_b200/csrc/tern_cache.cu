@@ -8,8 +8,8 @@
 // eight codes are one word of the K layout: 512 consecutive bytes leave per warp and store. V's words hold two tokens of
 // an entry: the eight lanes 8 q .. 8 q + 7 transpose their 8 x 8 codes (three exchanges), and lane 8 q + c then
 // stores what belongs to lane 4 c + q. Where tokens of a block are not new, V's half words are stored one by one.
-// Measured: append and read back of 4 x 4000 tokens, 8 heads of 128, 35 us of 147 MB (4.2 TB/s; the append issues in 68 % of the
-// slots); one token of 64 sequences 8 us, two launches of latency.
+// Measured: append and read back of 4 x 4000 tokens, 8 heads of 128, 35 us of 147 MB (4.2 TB/s), the append alone 20.5 (it issues in
+// 68 % of the slots; heads of 128 spill 8 bytes at 64 registers); one token of 64 sequences 8 us, two launches of latency.
 #include "tern_cache.cuh"
 
 namespace tern {

@@ -9,11 +9,10 @@
 //   O^T [D, 8 rows] += V^T [D, 16 tokens] P^T [16 tokens, 8 rows].
 // The cache's layout is that of the A operands, so codes go from memory to the instruction with no shuffle: a
 // word is four pairs (entries of a token for K, two tokens of an entry for V). P^T is S^T's
-// fragment transposed within the warp (movmatrix). With few rows this is bound by HBM, then by the issue
-// slots of the decoding.
-// P and V enter their product rounded to fp16, half a step each, which is of the size of the result's own rounding (3.4e-4 of
-// it in the norm, 2.1e-4 of that the last rounding). P in two parts would leave 2.8e-4 and was too dear: 64 sequences of
-// up to 8192 tokens 93.1 us against 84.4, 4 tokens over 131072 73.0 against 64.3. Scores, maxima, sums and O stay in fp32.
+// fragment transposed within the warp (movmatrix). With few rows its floor is HBM's.
+// P and V enter their product rounded to fp16, half a step each, which is of the size of the result's own rounding (3.0e-4 to
+// 3.5e-4 of it in the norm, 2.1e-4 of that the last rounding). P in two parts leaves 2.9e-4 and was too dear: 64 sequences of
+// up to 8192 tokens 87.6 us against 79.2, 4 tokens over 131072 59.4 against 52.3. Scores, maxima, sums and O stay in fp32.
 //
 // Work is split evenly whatever the lengths: the visible blocks of all (sequence, kv head, row tile), in pairs, in a
 // row are cut into equal ranges, one per CTA of a grid that fills the SMs once; every CTA finds its range from
@@ -22,8 +21,9 @@
 // shared memory. A (sequence, head, tile) that lies in one range is finished there; the pieces of one that
 // crosses ranges go to the workspace and a second, small kernel joins them, in the order of the ranges. Where no (sequence,
 // head, tile) can be long, by the table's width and the window, each has a CTA of its own instead.
-// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 79 us (4.2 TB/s), bound
-// by instruction issue (57 % of the slots, 300 warp instructions per block) and what each segment's start and join cost.
+// Measured (D = 128, one token, 4 heads per kv head): 64 sequences of up to 8192 tokens, 330 MB, 79 us (4.2 TB/s). Nothing is
+// full: 57 % of the issue slots (300 warp instructions per block), 52 % of DRAM, 26 % of the tensor pipe; the rest is waiting, in
+// the chains within a pair and in each segment's start and join, with 12 warps per SM.
 #include <math.h>
 
 #include <algorithm>
@@ -40,7 +40,9 @@ constexpr int kSplitWarps = 4;             // warps of a CTA where segments are 
 constexpr int kFewWarps = 8, kManyWarps = 16;   // and where each has a CTA of its own: many where every CTA has an SM to itself
                                            // (16 sequences of 8 kv heads, 300 tokens 7.3 us against 8.4, 1000 tokens 10.3 against
                                            // 13.4), few where not (64 sequences: 15.8 against 25.5, 26.2 against 35.6)
-constexpr int kDirectUnits = 36;           // units of a segment up to which it has (measured, 1 / 4 / 16 / 64 sequences of 8 kv heads:
+constexpr int kDirectUnits = 36;           // units of a segment up to which it has, whatever the segments' number: at 1000 tokens (32
+                                           // units) it costs one sequence 3 % and saves more of them 3 to 24 %, at 2000 (63) it mostly
+                                           // costs, between them is not measured (1 / 4 / 16 / 64 sequences of 8 kv heads:
                                            // 300 tokens 6.5 6.7 6.9 14.2 us against 8.3 8.8 10.4 16.5 split; 1000 tokens
                                            // 9.0 9.1 9.6 24.7 against 8.7 9.5 12.7 25.5; 2000 12.8 12.8 14.0 36.3
                                            // against 9.0 10.8 14.9 33.8)
@@ -367,9 +369,9 @@ struct Smem {
     float m[kWarps][kRows], l[kWarps][kRows], top[kRows];
 };
 
-// CTAs of an SM: what leaves each variant its registers without spills. (D = 128, 8 rows: four CTAs of 128 registers took as long
-// over long sequences and longer over short ones, 4 sequences of up to 4000 tokens 13.3 us against 12.0; 16 rows: three took
-// 65.5 us over 131072 tokens against 61.1.)
+// CTAs of an SM: what leaves each split variant its registers without spills. (D = 128, 8 rows: four CTAs of 128 registers took
+// as long over long sequences and longer over short ones, 4 sequences of up to 4000 tokens 13.3 us against 12.0; 16 rows: three took
+// 65.5 us over 131072 tokens against 61.1.) The direct ones of D = 128 and 8 rows have 128 registers and spill 24 bytes.
 constexpr int resident(int D, int nt, int direct) { return direct ? (nt == 1 && direct == kFewWarps ? 2 : 1) : (nt == 1 ? 4 : 3) - (D == 128); }
 
 // kDirect > 0: CTA i, of so many warps, takes the whole of segment i, and nothing is split or joined.

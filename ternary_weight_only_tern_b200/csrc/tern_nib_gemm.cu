@@ -316,8 +316,8 @@ struct Plan {
 // decoding (M = 2048, 12288 x 4096: 1400 with 256 rows and tokens, 815 with 128 rows; 64 tokens: 415, decoding), about 3000 for
 // a CTA's start and end; slices of K add a kernel (8000: half of that leads 400 tokens at group 32, 4096 x 4096, to slices that
 // take 29.2 us against 22.1) and their sums' way through memory. At group 32 the decoding has four times
-// group 128's scales to load and choose (512 tokens, 9728 x 2560: 34.8 us with 600 for it, 43.4 with 400, by the tiles it leads
-// to; 1024 tokens, 12288 x 4096: 96.9 against 120).
+// group 128's scales to load, and chooses among them by lane, for which its variants keep a local frame of 16 or 32 bytes
+// (512 tokens, 9728 x 2560: 34.8 us with 600 for it, 43.4 with 400, by the tiles it leads to; 1024 tokens, 12288 x 4096: 96.9 against 120).
 Plan plan_of(const tern_nib_weight& w, int64_t M) {
     const int KB = int(w.K / kGroup);
     const int64_t sms = sm_count();
